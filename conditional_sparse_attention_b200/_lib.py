@@ -1,4 +1,4 @@
-"""ctypes view of liboda.so (include/oda.h, include/oda_glue.h).
+"""ctypes view of liboda.so (include/*.h).
 
 Loading fails loudly: there is no fallback implementation of any entry point.
 """
@@ -20,8 +20,11 @@ STATUS = {0: "ODA_OK", 1: "ODA_ERR_INVALID_ARG", 2: "ODA_ERR_UNSUPPORTED", 3: "O
 DEVERR_PAGE_RANGE = 0x1
 DEVERR_POS_RANGE = 0x2
 DEVERR_WAIT_TIMEOUT = 0x4
+DEVERR_ROW_RANGE = 0x8
 MAX_BATCH = 256
 MAX_LAYERS = 64
+MAX_TREE = 64
+MAX_VOCAB = 262144
 
 
 class OdaConfig(ctypes.Structure):
@@ -103,6 +106,18 @@ _SIGS = {
                          c_void_p, c_void_p, ctypes.c_size_t, c_void_p], c_int32),
     "oda_commit": ([c_void_p, _P(OdaKVLayer), c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
                     c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p], c_int32),
+    "oda_append": ([c_void_p, _P(OdaKVLayer), c_int32, c_void_p, c_void_p, c_int64, c_int64, c_void_p,
+                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p], c_int32),
+    "oda_append_fp8": ([c_void_p, _P(OdaKV8Layer), c_int32, c_void_p, c_void_p, c_int64, c_int64, c_void_p,
+                        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p], c_int32),
+    "oda_attend_full_prompt": ([c_void_p, c_int32, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
+                                c_int64, c_void_p, c_void_p], c_int32),
+    "oda_attend_local_prompt": ([c_void_p, c_int32, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
+                                 c_int64, c_void_p, c_void_p], c_int32),
+    "oda_attend_full_tree": ([c_void_p, _P(OdaKVLayer), c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p,
+                              c_void_p, c_void_p, c_void_p, c_void_p, c_void_p], c_int32),
+    "oda_sample": ([c_void_p, c_int32, c_int32, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                    c_void_p, c_void_p, c_void_p], c_int32),
     "oda_snapshot": ([c_void_p, _P(OdaState), _P(OdaState), c_void_p], c_int32),
     "oda_restore": ([c_void_p, c_void_p, _P(OdaState), _P(OdaState), c_void_p], c_int32),
     "oda_cond_begin": ([c_void_p, c_void_p, c_void_p, _P(c_void_p)], c_int32),

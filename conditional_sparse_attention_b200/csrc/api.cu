@@ -1,6 +1,6 @@
 // C ABI entry points: argument validation, context scratch, conditional capture, graphs,
-// error reporting.  Every compute step is one of the kernels in attention.cu, head.cu,
-// commit.cu and glue.cu.
+// error reporting.  Every compute step is one of the kernels in attention.cu, tile_attention.cu,
+// head.cu, commit.cu, sample.cu, backbone.cu and glue.cu.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
@@ -107,7 +107,7 @@ oda_status dev_alloc(T** p, size_t n, const char* what) {
 
 void free_ctx(oda_ctx* c) {
   if (!c) return;
-  void* ptrs[] = {c->part_o, c->part_ml, c->attn_cnt, c->err, c->head_part, c->head_ss,
+  void* ptrs[] = {c->tile_part_o, c->tile_part_ml, c->tile_plan, c->part_o, c->part_ml, c->attn_cnt, c->err, c->head_part, c->head_ss,
                   c->head_cnt, c->head_u, c->head_f, c->head_act, c->glue_x, c->glue_ss,
                   c->glue_cnt, c->bb_part, c->bb_cnt};
   for (void* p : ptrs)
@@ -163,6 +163,8 @@ oda_status oda_create(const oda_config* cfg, oda_ctx** out) {
                     "cudaDeviceGetAttribute");
   if (st == ODA_OK) st = oda::prepare_attention_kernel(x->g, x->n_sms, x->attn_ctas);
   if (st == ODA_OK) st = oda::prepare_head_kernel();
+  if (st == ODA_OK) st = oda::prepare_tile_attention();
+  if (st == ODA_OK) st = oda::prepare_sample_kernel();
   if (st != ODA_OK) {
     free_ctx(x);
     return st;
@@ -181,6 +183,10 @@ oda_status oda_create(const oda_config* cfg, oda_ctx** out) {
   if (st == ODA_OK) st = dev_alloc(&x->head_u, (size_t)3 * B * 1024, "cudaMalloc(head)");
   if (st == ODA_OK) st = dev_alloc(&x->head_f, (size_t)3 * B * 1024, "cudaMalloc(head)");
   if (st == ODA_OK) st = dev_alloc(&x->head_act, (size_t)B * 2048, "cudaMalloc(head)");
+  const size_t tile_rows = oda::tile_part_rows(x->n_sms);
+  if (st == ODA_OK) st = dev_alloc(&x->tile_part_o, tile_rows * 128, "cudaMalloc(tree partials)");
+  if (st == ODA_OK) st = dev_alloc(&x->tile_part_ml, tile_rows * 2, "cudaMalloc(tree partials)");
+  if (st == ODA_OK) st = dev_alloc(&x->tile_plan, (size_t)B + 1, "cudaMalloc(tree plan)");
   if (st == ODA_OK) st = dev_alloc(&x->glue_x, (size_t)B * D, "cudaMalloc(glue)");
   if (st == ODA_OK) st = dev_alloc(&x->glue_ss, (size_t)B * gch, "cudaMalloc(glue)");
   if (st == ODA_OK) st = dev_alloc(&x->glue_cnt, (size_t)2 * B, "cudaMalloc(glue)");
@@ -330,6 +336,73 @@ oda_status oda_commit_fp8(oda_ctx* ctx, const oda_kv8_layer* layers, int32_t n_l
   return oda::launch_commit(ctx, pools, n_layers, page_table, pos, flag, k_stage_local,
                             v_stage_local, k_stage_full, v_stage_full, h_local, h_full, h_prev,
                             stream);
+}
+
+static oda_status append_pools(oda_ctx* ctx, const void* layers, int32_t n_layers) {
+  if (!ctx) return set_error(ODA_ERR_INVALID_ARG, "append: ctx is NULL");
+  if (!layers || n_layers < 1 || n_layers > ODA_MAX_LAYERS)
+    return set_error(ODA_ERR_INVALID_ARG, "append: n_layers must be 1..%d", ODA_MAX_LAYERS);
+  return ODA_OK;
+}
+
+oda_status oda_append(oda_ctx* ctx, const oda_kv_layer* layers, int32_t n_layers,
+                      const int32_t* page_table, const int32_t* pos, int64_t n_rows, int64_t n_stage,
+                      const int32_t* cu_rows, const int32_t* rows, const void* k_stage,
+                      const void* v_stage, const float* h_stage, float* h_prev, int32_t* pos_next,
+                      cudaStream_t stream) {
+  oda_status st = append_pools(ctx, layers, n_layers);
+  if (st != ODA_OK) return st;
+  oda::KvPool pools[ODA_MAX_LAYERS];
+  for (int l = 0; l < n_layers; ++l) pools[l] = {0, layers[l].k, layers[l].v, layers[l].n_pages};
+  return oda::launch_append(ctx, pools, n_layers, page_table, pos, n_rows, n_stage, cu_rows, rows,
+                            k_stage, v_stage, h_stage, h_prev, pos_next, stream);
+}
+
+oda_status oda_append_fp8(oda_ctx* ctx, const oda_kv8_layer* layers, int32_t n_layers,
+                          const int32_t* page_table, const int32_t* pos, int64_t n_rows,
+                          int64_t n_stage, const int32_t* cu_rows, const int32_t* rows,
+                          const void* k_stage, const void* v_stage, const float* h_stage,
+                          float* h_prev, int32_t* pos_next, cudaStream_t stream) {
+  oda_status st = append_pools(ctx, layers, n_layers);
+  if (st != ODA_OK) return st;
+  oda::KvPool pools[ODA_MAX_LAYERS];
+  for (int l = 0; l < n_layers; ++l) pools[l] = {1, layers[l].kv, nullptr, layers[l].n_pages};
+  return oda::launch_append(ctx, pools, n_layers, page_table, pos, n_rows, n_stage, cu_rows, rows,
+                            k_stage, v_stage, h_stage, h_prev, pos_next, stream);
+}
+
+oda_status oda_attend_full_prompt(oda_ctx* ctx, int32_t n_seqs, int64_t n_rows,
+                                  const int32_t* cu_rows, const void* q, const void* k,
+                                  const void* v, int64_t q_stride, int64_t kv_stride, void* out,
+                                  cudaStream_t stream) {
+  if (!ctx) return set_error(ODA_ERR_INVALID_ARG, "attend_full_prompt: ctx is NULL");
+  return oda::launch_prompt(ctx, n_seqs, n_rows, cu_rows, q, k, v, q_stride, kv_stride, out, 0, stream);
+}
+
+oda_status oda_attend_local_prompt(oda_ctx* ctx, int32_t n_seqs, int64_t n_rows,
+                                   const int32_t* cu_rows, const void* q, const void* k,
+                                   const void* v, int64_t q_stride, int64_t kv_stride, void* out,
+                                   cudaStream_t stream) {
+  if (!ctx) return set_error(ODA_ERR_INVALID_ARG, "attend_local_prompt: ctx is NULL");
+  return oda::launch_prompt(ctx, n_seqs, n_rows, cu_rows, q, k, v, q_stride, kv_stride, out, 1, stream);
+}
+
+oda_status oda_attend_full_tree(oda_ctx* ctx, const oda_kv_layer* layer, const int32_t* page_table,
+                                const int32_t* pos, const int32_t* flag, int64_t n_rows,
+                                const int32_t* cu_rows, const int32_t* parent, const void* q,
+                                const void* k_new, const void* v_new, void* out,
+                                cudaStream_t stream) {
+  if (!ctx) return set_error(ODA_ERR_INVALID_ARG, "attend_full_tree: ctx is NULL");
+  return oda::launch_tree(ctx, layer, page_table, pos, flag, n_rows, cu_rows, parent, q, k_new, v_new, out, stream);
+}
+
+oda_status oda_sample(oda_ctx* ctx, int32_t n_rows, int32_t vocab, int64_t row_stride,
+                      const float* logits, const float* temperature, const int32_t* top_k,
+                      const float* top_p, const float* min_p, const float* u, int32_t* token,
+                      float* prob, cudaStream_t stream) {
+  if (!ctx) return set_error(ODA_ERR_INVALID_ARG, "sample: ctx is NULL");
+  return oda::launch_sample(ctx, n_rows, vocab, row_stride, logits, temperature, top_k, top_p, min_p, u,
+                            token, prob, stream);
 }
 
 oda_status oda_snapshot(oda_ctx* ctx, const oda_state* live, const oda_state* snap,

@@ -134,6 +134,129 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitParams p) {
   }
 }
 
+struct AppendParams {
+  void* k[ODA_MAX_LAYERS];
+  void* v[ODA_MAX_LAYERS];
+  int64_t n_pages[ODA_MAX_LAYERS];
+  const int32_t* page_table;
+  const int32_t* pos;
+  const int32_t* cu;
+  const int32_t* rows;
+  const uint4* ks;        // staging [L][n_stage][Hkv][128] bf16 as 16-byte words
+  const uint4* vs;
+  const float4* h;
+  float4* h_prev;
+  int32_t* pos_next;
+  int32_t* err;
+  int64_t n_rows, n_stage;
+  int B, Hkv, max_pages, D4;
+};
+
+__device__ __forceinline__ bool append_bounds(const AppendParams& p, int b, int* a, int* e) {
+  *a = p.cu[b];
+  *e = p.cu[b + 1];
+  return *a >= 0 && *e >= *a && (int64_t)*e <= p.n_rows;
+}
+
+// Where one appended row goes: its staging row, and page and slot of its position; src < 0: nowhere.
+struct AppendTo {
+  int src, phys, slot;
+};
+
+// The sequence of row i is searched by a warp (sequences with bad bounds hold no rows).
+__device__ __forceinline__ AppendTo append_to(const AppendParams& p, int64_t i, int lane, bool report) {
+  AppendTo t = {-1, 0, 0};
+  int b = -1;
+  for (int b0 = 0; b0 < p.B && b < 0; b0 += 32) {
+    int a = 0, e = 0;
+    const int x = b0 + lane;
+    const bool in = x < p.B && append_bounds(p, x, &a, &e) && a <= i && i < e;
+    const uint32_t here = __ballot_sync(0xffffffffu, in);
+    if (here) b = b0 + __ffs((int)here) - 1;
+  }
+  if (b < 0) return t;
+  const int first = p.pos[b];
+  const int64_t at = (int64_t)first - 1 + (i - p.cu[b]);        // 0-based place in the cache
+  if (first < 1 || at >= (int64_t)p.max_pages * kPageTok) {
+    if (report && lane == 0) atomicOr(p.err, ODA_DEVERR_POS_RANGE);
+    return t;
+  }
+  const int64_t src = p.rows ? p.rows[i] : i;
+  if (src < 0 || src >= p.n_stage) {
+    if (report && lane == 0) atomicOr(p.err, ODA_DEVERR_ROW_RANGE);
+    return t;
+  }
+  t.phys = p.page_table[(size_t)b * p.max_pages + at / kPageTok];
+  t.slot = (int)(at % kPageTok);
+  t.src = (int)src;
+  return t;
+}
+
+constexpr int kAppendRows = 16;
+
+// One CTA writes kAppendRows consecutive rows of one layer (blockIdx.y).
+template <int F>
+__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+  __shared__ AppendTo to[kAppendRows];
+  const int l = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t i0 = (int64_t)blockIdx.x * kAppendRows;
+  for (int j = warp; j < kAppendRows; j += 8) {
+    AppendTo t = {-1, 0, 0};
+    if (i0 + j < p.n_rows) t = append_to(p, i0 + j, lane, l == 0);
+    if (t.src >= 0 && (t.phys < 0 || (int64_t)t.phys >= p.n_pages[l])) {
+      if (lane == 0) atomicOr(p.err, ODA_DEVERR_PAGE_RANGE);
+      t.src = -1;
+    }
+    if (lane == 0) to[j] = t;
+  }
+  __syncthreads();
+  const int words = p.Hkv * 16;   // 16-byte words per row of K or V
+  if constexpr (F == 0) {
+    for (int x = threadIdx.x; x < kAppendRows * 2 * words; x += blockDim.x) {
+      const int j = x / (2 * words), y = x - j * 2 * words;
+      const int which = y >= words, w = y - which * words;
+      const AppendTo t = to[j];
+      if (t.src < 0) continue;
+      const uint4 val = (which ? p.vs : p.ks)[((size_t)l * p.n_stage + t.src) * words + w];
+      uint4* pool = reinterpret_cast<uint4*>(which ? p.v[l] : p.k[l]);
+      pool[(((size_t)t.phys * p.Hkv + (w >> 4)) * kPageTok + t.slot) * 16 + (w & 15)] = val;
+    }
+  } else {
+    for (int x = warp; x < kAppendRows * 2 * p.Hkv; x += 8) {
+      const int j = x / (2 * p.Hkv), y = x - j * 2 * p.Hkv;
+      const int which = y >= p.Hkv, h = y - which * p.Hkv;
+      const AppendTo t = to[j];
+      if (t.src < 0) continue;
+      const uint2 wv = reinterpret_cast<const uint2*>(which ? p.vs : p.ks)[(((size_t)l * p.n_stage + t.src) * words + h * 16) * 2 + lane];
+      float sc;
+      const uint32_t codes = quantize_row_e4m3(wv.x, wv.y, lane, &sc);
+      store_row_e4m3(static_cast<uint8_t*>(p.k[l]) + ((size_t)t.phys * p.Hkv + h) * kF8Block, which, t.slot, codes, sc, lane);
+    }
+  }
+}
+
+// After every row is written: the hidden state of each sequence's last row, and its next position.
+__global__ void __launch_bounds__(256) append_finish_kernel(const AppendParams p) {
+  grid_dependency_wait();
+  const int b = blockIdx.x;
+  int a, e;
+  const bool ok = append_bounds(p, b, &a, &e);
+  const int t = p.pos[b];
+  if (threadIdx.x == 0 && !ok) atomicOr(p.err, ODA_DEVERR_ROW_RANGE);
+  if (!ok || t < 1) {
+    __syncthreads();
+    if (threadIdx.x == 0 && p.pos_next) p.pos_next[b] = t;
+    return;
+  }
+  if (p.h_prev && e > a) {
+    const int64_t src = p.rows ? p.rows[e - 1] : e - 1;
+    if (src >= 0 && src < p.n_stage)
+      for (int i = threadIdx.x; i < p.D4; i += blockDim.x) p.h_prev[(size_t)b * p.D4 + i] = p.h[(size_t)src * p.D4 + i];
+  }
+  __syncthreads();                // every thread has read pos[b], which pos_next may be
+  if (threadIdx.x == 0 && p.pos_next) p.pos_next[b] = t + (e - a);
+}
+
 // dst[b] <- src[b] for every sequence (flag == nullptr) or the flagged ones; blockIdx.y = b.
 __global__ void state_copy_kernel(const float4* src, float4* dst, size_t per_seq4,
                                   const int32_t* flag) {
@@ -226,6 +349,70 @@ oda_status launch_commit(oda_ctx* ctx, const KvPool* layers, int32_t n_layers,
   else
     commit_kernel<1><<<dim3(n_layers, cf.batch), 256, 0, stream>>>(p);
   return check_cuda(cudaGetLastError(), "commit launch");
+}
+
+oda_status launch_append(oda_ctx* ctx, const KvPool* layers, int32_t n_layers, const int32_t* page_table,
+                         const int32_t* pos, int64_t n_rows, int64_t n_stage, const int32_t* cu_rows,
+                         const int32_t* rows, const void* k_stage, const void* v_stage, const float* h_stage,
+                         float* h_prev, int32_t* pos_next, cudaStream_t stream) {
+  const oda_config& cf = ctx->cfg;
+  const int F = layers[0].fmt;
+  if (!page_table || !pos || !cu_rows || !k_stage || !v_stage)
+    return set_error(ODA_ERR_INVALID_ARG, "append: null pointer argument");
+  if ((h_stage == nullptr) != (h_prev == nullptr))
+    return set_error(ODA_ERR_INVALID_ARG, "append: h_stage and h_prev go together");
+  if (n_rows < 0 || n_rows > INT32_MAX || n_stage < 1 || n_stage > INT32_MAX || (!rows && n_rows > n_stage))
+    return set_error(ODA_ERR_INVALID_ARG, "append: n_rows or n_stage out of range");
+  const void* al[] = {k_stage, v_stage, h_stage, h_prev};
+  for (const void* q : al)
+    if (reinterpret_cast<uintptr_t>(q) & 15)
+      return set_error(ODA_ERR_INVALID_ARG, "append: staging and hidden buffers must be 16-byte aligned");
+  AppendParams p;
+  for (int l = 0; l < n_layers; ++l) {
+    if (!layers[l].k || (F == 0 && !layers[l].v) || layers[l].n_pages <= 0 ||
+        ((reinterpret_cast<uintptr_t>(layers[l].k) | reinterpret_cast<uintptr_t>(layers[l].v)) & 15))
+      return set_error(ODA_ERR_INVALID_ARG, "append: bad KV pool of layer %d", l);
+    p.k[l] = const_cast<void*>(layers[l].k);
+    p.v[l] = const_cast<void*>(layers[l].v);
+    p.n_pages[l] = layers[l].n_pages;
+  }
+  p.page_table = page_table;
+  p.pos = pos;
+  p.cu = cu_rows;
+  p.rows = rows;
+  p.ks = static_cast<const uint4*>(k_stage);
+  p.vs = static_cast<const uint4*>(v_stage);
+  p.h = reinterpret_cast<const float4*>(h_stage);
+  p.h_prev = reinterpret_cast<float4*>(h_prev);
+  p.pos_next = pos_next;
+  p.err = ctx->err;
+  p.n_rows = n_rows;
+  p.n_stage = n_stage;
+  p.B = cf.batch;
+  p.Hkv = cf.n_kv_heads;
+  p.max_pages = cf.max_pages;
+  p.D4 = cf.head_in_dim / 4;
+  ctx->prev_attention = false;
+  oda_status st = ODA_OK;
+  if (n_rows > 0) {
+    const dim3 grid((unsigned)((n_rows + kAppendRows - 1) / kAppendRows), n_layers);
+    if (F == 0)
+      append_kernel<0><<<grid, 256, 0, stream>>>(p);
+    else
+      append_kernel<1><<<grid, 256, 0, stream>>>(p);
+    st = check_cuda(cudaGetLastError(), "append launch");
+    if (st != ODA_OK) return st;
+  }
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(cf.batch);
+  lc.blockDim = dim3(256);
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return check_cuda(cudaLaunchKernelEx(&lc, append_finish_kernel, p), "append finish launch");
 }
 
 oda_status launch_state_copy(const oda_state* src, const oda_state* dst, int B,

@@ -7,6 +7,7 @@
 #include "oda.h"
 #include "oda_glue.h"
 #include "oda_backbone.h"
+#include "oda_serve.h"
 
 struct oda_ctx {
   oda_config cfg;
@@ -32,6 +33,11 @@ struct oda_ctx {
   size_t bb_part_floats = 0;
   int32_t* bb_cnt = nullptr;
   int bb_cnt_n = 0;
+  // prompt and tree attention: partial results [2 SMs][256][128] with (reference, sum) pairs, and
+  // the tiles before each sequence [B + 1]
+  float* tile_part_o = nullptr;
+  float* tile_part_ml = nullptr;
+  uint32_t* tile_plan = nullptr;
   // glue scratch
   float* glue_x = nullptr;      // [B][D]
   float* glue_ss = nullptr;     // [B][chunks]
@@ -79,6 +85,22 @@ oda_status launch_attention_noalloc(const oda_config* cfg, const oda_kv_layer* l
                                     const void* v_new, float* out, int32_t* device_error,
                                     cudaStream_t stream);
 
+// tile_attention.cu
+size_t tile_part_rows(int n_sms);
+oda_status prepare_tile_attention();
+oda_status launch_prompt(oda_ctx* ctx, int n_seqs, int64_t n_rows, const int32_t* cu_rows, const void* q,
+                         const void* k, const void* v, int64_t q_stride, int64_t kv_stride, void* out, int local,
+                         cudaStream_t stream);
+oda_status launch_tree(oda_ctx* ctx, const oda_kv_layer* layer, const int32_t* page_table, const int32_t* pos,
+                       const int32_t* flag, int64_t n_rows, const int32_t* cu_rows, const int32_t* parent,
+                       const void* q, const void* k_new, const void* v_new, void* out, cudaStream_t stream);
+
+// sample.cu
+oda_status prepare_sample_kernel();
+oda_status launch_sample(oda_ctx* ctx, int n_rows, int vocab, int64_t row_stride, const float* logits,
+                         const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                         const float* u, int32_t* token, float* prob, cudaStream_t stream);
+
 // head.cu
 oda_status launch_recall_head(oda_ctx* ctx, const oda_head_weights* w, const float* h_prev,
                               const float* emb, const float* h_loc, const int32_t* sched,
@@ -104,6 +126,10 @@ oda_status launch_commit(oda_ctx* ctx, const KvPool* layers, int32_t n_layers,
                          const void* ksl, const void* vsl, const void* ksf, const void* vsf,
                          const float* h_local, const float* h_full, float* h_prev,
                          cudaStream_t stream);
+oda_status launch_append(oda_ctx* ctx, const KvPool* layers, int32_t n_layers, const int32_t* page_table,
+                         const int32_t* pos, int64_t n_rows, int64_t n_stage, const int32_t* cu_rows,
+                         const int32_t* rows, const void* k_stage, const void* v_stage, const float* h_stage,
+                         float* h_prev, int32_t* pos_next, cudaStream_t stream);
 oda_status launch_state_copy(const oda_state* src, const oda_state* dst, int B,
                              const int32_t* flag, cudaStream_t stream);
 

@@ -1,0 +1,895 @@
+// Attention of many query rows per KV head on the fifth-generation tensor cores: whole prompts
+// (packed sequences, full or local set) and trees of drafted tokens over the paged cache.
+//
+// Mathematics: for a query row q with visible set S, o = sum_{j in S} p_j v_j / sum_{j in S} p_j with
+// p_j = 2^(c (q.k_j - m)), c = log2(e) / sqrt(128), m a running reference that is at least the running
+// maximum less 8 / c, so 2^8 bounds p and the reference moves (and O is rescaled) only where the
+// maximum has grown by more than that.
+//
+// One CTA works on two "slots" of 128 query rows that share the KV head and its K/V tiles of 128
+// positions.  A slot's rows are (token, head of the group) pairs, 128 / g tokens x g heads, so a KV tile
+// is read once for all heads of its group and a short prompt or a small tree still fills the rows.
+// Where only slot 0 has tokens, slot 1 takes every second KV tile of the same rows and the two partial
+// results are joined through tensor memory at the end: the two slots always alternate on the tensor
+// cores, one computing weights while the other's products run.
+//
+//   warps 0-3, 4-7: one thread per row of slot 0 / 1: scores from TMEM, weights back to TMEM as bf16
+//   warp 8:         issues the products S = Q K^T and O += P V (M = N = 128, 16-deep steps)
+//   warp 9:         brings Q, K and V by TMA (5 stages of 32 KB for K and V tiles)
+//   warps 10, 11:   idle (they complete the warpgroup whose registers go to the other two)
+//
+// TMEM: S0 | S1 | O0 | O1, 128 columns each; P_i overwrites the first 64 columns of S_i.
+// Every wait is bounded; a wait that gives up sets ODA_DEVERR_WAIT_TIMEOUT and ends the CTA.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "tc5.cuh"
+
+namespace oda {
+namespace {
+
+constexpr int kTile = 128;              // query rows of a slot; positions of a KV tile
+constexpr int kStages = 5;
+constexpr int kStageBytes = kTile * 256;
+constexpr int kHalf = kTile * 128;      // bytes of one 64-value half of a tile
+constexpr int kThreads = 384;           // 168 registers a thread at launch, then 208 / 208 / 88 by warpgroup
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kGrow = 8.0f;           // log2 of the growth that moves a row's reference
+constexpr uint32_t kColS = 0, kColO = 256;
+
+struct TileParams {
+  const int32_t* cu;
+  __nv_bfloat16* out;
+  int32_t* err;
+  int64_t n_rows;
+  int n_seqs, Hq, Hkv, g, nt;           // nt = tokens of a slot
+  int local, sinks, window;
+  float c;                              // log2(e) / sqrt(128)
+  // tree
+  const int32_t* page_table;
+  const int32_t* pos;
+  const int32_t* flag;
+  const int32_t* parent;
+  int64_t n_pages;
+  int max_pages;
+  float* part_o;                        // [2 grid][256][128]
+  float* part_ml;                       // [2 grid][256][2]
+  uint32_t* plan;                       // [n_seqs + 1] tiles before each sequence
+};
+
+struct Smem {
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t m_ready, m_done;
+  float2 other[kTile];                  // slot 1's reference and sum where the slots are joined
+  uint32_t tmem;
+  uint32_t pref[ODA_MAX_BATCH + 1];     // prompt: blocks of each sequence; tree: tiles before it
+};
+constexpr int kTileBytes = (2 + kStages) * kStageBytes;   // Q slots, then K and V stages
+constexpr int kDynBytes = kTileBytes + sizeof(Smem);
+static_assert(kDynBytes <= 227 * 1024, "shared memory of a CTA");
+
+// A CTA's unit of work: up to two slots of one KV head against a run of KV tiles.
+struct Job {
+  int b, h;            // sequence, KV head
+  int row0;            // packed row of the sequence's first token or node
+  int len;             // its tokens or nodes
+  int tok0;            // first token of slot 0
+  int n[2];            // valid tokens of each slot
+  int first, sink;     // KV tile of step s: s == 0 && sink ? 0 : first + s - sink
+  int steps[2];        // steps of each slot (dual: of the job)
+  int total;
+  int dual;
+  int cached;          // tree: cached positions; prompt: unused
+  int node_tile;       // tree: the KV tile that holds the nodes; prompt: -1
+  int direct;          // result complete: write out, else a partial
+  int part;            // partial slot
+};
+__device__ __forceinline__ int kv_tile(const Job& j, int s) { return (j.sink && s == 0) ? 0 : j.first + s - j.sink; }
+__device__ __forceinline__ bool active(const Job& j, int i, int s) { return j.dual ? (s & 1) == i : s < j.steps[i]; }
+__device__ __forceinline__ int slot_steps(const Job& j, int i) { return j.dual ? (j.total + 1 - i) >> 1 : j.steps[i]; }
+
+__device__ __forceinline__ int seq_len(const TileParams& p, int b, int most, bool report) {
+  const int a = p.cu[b], e = p.cu[b + 1];
+  if (a < 0 || e < a || (int64_t)e > p.n_rows || e - a > most) {
+    if (report) atomicOr(p.err, ODA_DEVERR_ROW_RANGE);
+    return 0;
+  }
+  return e - a;
+}
+
+// Prompt work: block j of a sequence is its tokens [2 nt j, 2 nt (j + 1)); units are (block, KV head),
+// ordered by falling block index over all sequences (the longest rows first), KV heads innermost.
+// pref holds every sequence's block count.  Called by a whole warp.
+__device__ __forceinline__ uint32_t blocks_from(const Smem& sm, int n_seqs, uint32_t j, int lane) {
+  uint32_t s = 0;
+  for (int b = lane; b < n_seqs; b += 32) {
+    const uint32_t nb = sm.pref[b];
+    s += nb > j ? nb - j : 0u;
+  }
+  return __reduce_add_sync(0xffffffffu, s);
+}
+
+__device__ __forceinline__ bool prompt_job(const TileParams& p, const Smem& sm, uint32_t id, int lane, Job& jb) {
+  const uint32_t rank = id / (uint32_t)p.Hkv;
+  uint32_t most = 0;
+  for (int b = lane; b < p.n_seqs; b += 32) most = max(most, sm.pref[b]);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (rank >= blocks_from(sm, p.n_seqs, 0, lane)) return false;
+  uint32_t lo = 0, hi = most;            // blocks_from(lo) > rank >= blocks_from(hi)
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) >> 1;
+    if (blocks_from(sm, p.n_seqs, mid, lane) > rank) lo = mid;
+    else hi = mid;
+  }
+  uint32_t k = rank - blocks_from(sm, p.n_seqs, lo + 1, lane);
+  int b = 0;
+  for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
+    const uint32_t here = __ballot_sync(0xffffffffu, b0 + lane < p.n_seqs && sm.pref[b0 + lane] > lo);
+    const uint32_t cnt = __popc(here);
+    if (k < cnt) {
+      b = b0 + (int)__fns(here, 0, (int)k + 1);
+      break;
+    }
+    k -= cnt;
+  }
+  jb.b = b;
+  jb.h = (int)(id % (uint32_t)p.Hkv);
+  jb.row0 = p.cu[b];
+  jb.len = p.cu[b + 1] - jb.row0;
+  jb.tok0 = (int)lo * 2 * p.nt;
+  jb.n[0] = min(p.nt, jb.len - jb.tok0);
+  jb.n[1] = max(0, min(p.nt, jb.len - jb.tok0 - p.nt));
+  jb.first = 0;
+  if (p.local && jb.tok0 >= p.window) jb.first = (jb.tok0 - p.window + 1) / kTile;
+  jb.sink = (p.local && p.sinks > 0 && jb.first > 0) ? 1 : 0;
+  jb.steps[0] = (jb.tok0 + jb.n[0] - 1) / kTile - jb.first + 1 + jb.sink;
+  jb.steps[1] = jb.n[1] > 0 ? (jb.tok0 + p.nt + jb.n[1] - 1) / kTile - jb.first + 1 + jb.sink : 0;
+  jb.total = max(jb.steps[0], jb.steps[1]);
+  jb.dual = jb.n[1] == 0 && jb.total > 1;
+  jb.node_tile = -1;
+  jb.cached = 0;
+  jb.direct = 1;
+  jb.part = 0;
+  return true;
+}
+
+// Tree work: sequence b has M = ceil(nodes / 2 nt) units per KV head, each of `tiles` KV tiles
+// (the cached positions', then one for the nodes).  All tiles of all units, in the order
+// (sequence, KV head, unit), are cut into equal runs, one for each CTA; `at` walks this CTA's run.
+__device__ __forceinline__ bool tree_job(const TileParams& p, const Smem& sm, uint32_t& at, uint32_t begin,
+                                         uint32_t end, Job& jb) {
+  if (at >= end) return false;
+  int lo = 0, hi = p.n_seqs;             // pref[lo] <= at < pref[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sm.pref[mid] <= at) lo = mid;
+    else hi = mid;
+  }
+  const int b = lo;
+  jb.b = b;
+  jb.row0 = p.cu[b];
+  jb.len = p.cu[b + 1] - jb.row0;
+  jb.cached = p.pos[b] - 1;
+  const uint32_t tiles = (uint32_t)((jb.cached + kTile - 1) / kTile + 1);
+  const uint32_t M = (uint32_t)((jb.len + 2 * p.nt - 1) / (2 * p.nt));
+  const uint32_t rel = at - sm.pref[b];
+  const uint32_t u = rel / tiles, j0 = rel - u * tiles;
+  const uint32_t j1 = min(tiles, j0 + (end - at));
+  jb.h = (int)(u / M);
+  jb.tok0 = (int)(u % M) * 2 * p.nt;
+  jb.n[0] = min(p.nt, jb.len - jb.tok0);
+  jb.n[1] = max(0, min(p.nt, jb.len - jb.tok0 - p.nt));
+  jb.first = (int)j0;
+  jb.sink = 0;
+  jb.total = (int)(j1 - j0);
+  jb.steps[0] = jb.total;
+  jb.steps[1] = jb.n[1] > 0 ? jb.total : 0;
+  jb.dual = jb.n[1] == 0 && jb.total > 1;
+  jb.node_tile = (int)tiles - 1;
+  jb.direct = j0 == 0 && j1 == tiles;
+  jb.part = 2 * (int)blockIdx.x + (at == begin ? 0 : 1);
+  at += j1 - j0;
+  return true;
+}
+
+// Walks the CTA's jobs; every warp walks them by itself.
+template <bool TREE>
+struct Walk {
+  uint32_t at, begin, end, stride;
+  __device__ Walk(const TileParams& p, const Smem& sm) {
+    if (TREE) {
+      const uint32_t W = sm.pref[p.n_seqs];
+      const uint32_t share = (W + gridDim.x - 1) / gridDim.x;
+      begin = min(W, share * blockIdx.x);
+      end = min(W, begin + share);
+      at = begin;
+      stride = 0;
+    } else {
+      at = blockIdx.x;
+      begin = end = 0;
+      stride = gridDim.x;
+    }
+  }
+  __device__ bool next(const TileParams& p, const Smem& sm, int lane, Job& j) {
+    if (TREE) return tree_job(p, sm, at, begin, end, j);
+    if (!prompt_job(p, sm, at, lane, j)) return false;
+    at += stride;
+    return true;
+  }
+};
+
+// Low `n` bits (n may be <= 0 or >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// Nodes that node `i` of a tree of at most 64 sees: its ancestors and itself.
+__device__ __forceinline__ uint64_t ancestors(const int32_t* parent, int i, int32_t* err) {
+  uint64_t m = 0;
+  while (true) {
+    m |= 1ull << i;
+    const int up = parent[i];
+    if (up < -1 || up >= i) {
+      atomicOr(err, ODA_DEVERR_ROW_RANGE);
+      break;
+    }
+    if (up < 0) break;
+    i = up;                              // falls at every turn: at most 64 turns
+  }
+  return m;
+}
+
+__device__ __forceinline__ void pin32(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+template <bool TREE>
+__global__ void __launch_bounds__(kThreads, 1)
+tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mkn,
+                      const __grid_constant__ CUtensorMap mvn, const TileParams p) {
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  Smem& sm = *reinterpret_cast<Smem*>(dyn + kTileBytes);
+  uint8_t* sq = dyn;                                    // two slots of Q
+  uint8_t* skv = dyn + 2 * kStageBytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.kv_full[i], 1);
+      mbar_init(&sm.kv_empty[i], 1);
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], kTile);
+      mbar_init(&sm.o_full[i], 1);
+    }
+    mbar_init(&sm.m_ready, kTile);
+    mbar_init(&sm.m_done, kTile);
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(&sm.tmem, 512);
+  if (TREE) {
+    // tiles before each sequence: one warp, 32 sequences at a time
+    if (warp == 9) {
+      uint32_t run = 0;
+      for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        uint32_t w = 0;
+        if (b < p.n_seqs && (!p.flag || p.flag[b] != 0)) {
+          const int n = seq_len(p, b, ODA_MAX_TREE, blockIdx.x == 0);
+          const int t = p.pos[b];
+          const bool ok = t >= 1 && (int64_t)(t - 1) <= (int64_t)p.max_pages * 16;
+          if (!ok && blockIdx.x == 0) atomicOr(p.err, ODA_DEVERR_POS_RANGE);
+          if (ok && n > 0)
+            w = (uint32_t)((t - 1 + kTile - 1) / kTile + 1) * (uint32_t)((n + 2 * p.nt - 1) / (2 * p.nt)) * (uint32_t)p.Hkv;
+        }
+        uint32_t inc = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += x;
+        }
+        if (b < p.n_seqs) sm.pref[b] = run + inc - w;
+        run += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      if (lane == 0) sm.pref[p.n_seqs] = run;
+      __syncwarp();
+      if (blockIdx.x == 0)
+        for (int b = lane; b <= p.n_seqs; b += 32) p.plan[b] = sm.pref[b];
+    }
+  } else {
+    for (int b = tid; b < p.n_seqs; b += kThreads)
+      sm.pref[b] = (uint32_t)((seq_len(p, b, 0x7fffffff, blockIdx.x == 0) + 2 * p.nt - 1) / (2 * p.nt));
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  Walk<TREE> walk(p, sm);
+  Job jb;
+  bool ok = true;
+
+  // the registers of the launch, 128 x (168 x 3), split 128 x (208 + 208 + 88)
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 9) {
+    // ------------------------------------------------------------------ loads
+    uint32_t gs = 0, jobs = 0;           // KV tiles (K, V counted apart: 2 gs) and jobs so far
+    while (ok && walk.next(p, sm, lane, jb)) {
+      if (jobs > 0) ok = mbar_wait_bounded(&sm.q_empty, (jobs - 1) & 1, kWaitNs);
+      if (!ok) break;
+      if (lane == 0) {
+        const int slots = jb.n[1] > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(slots * 2 * 128 * p.g * p.nt));
+        for (int i = 0; i < slots; ++i)
+          for (int hf = 0; hf < 2; ++hf)
+            tma_load_3d(sq + i * kStageBytes + hf * kHalf, &mq, hf * 64, jb.h * p.g, jb.row0 + jb.tok0 + i * p.nt,
+                        &sm.q_full);
+      }
+      ++jobs;
+      for (int s = 0; s < jb.total && ok; ++s, ++gs) {
+        const int t = kv_tile(jb, s);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t n = 2 * gs + w, st = n % kStages;
+          if (n >= kStages) ok = mbar_wait_bounded(&sm.kv_empty[st], (n / kStages - 1) & 1, kWaitNs);
+          if (!ok) break;
+          uint8_t* dst = skv + st * kStageBytes;
+          if (!TREE) {
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&sm.kv_full[st], kStageBytes);
+              for (int hf = 0; hf < 2; ++hf)
+                tma_load_3d(dst + hf * kHalf, w ? &mv : &mk, hf * 64, jb.h, jb.row0 + t * kTile, &sm.kv_full[st]);
+            }
+          } else if (t == jb.node_tile) {
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&sm.kv_full[st], ODA_MAX_TREE * 256);
+              for (int hf = 0; hf < 2; ++hf)
+                tma_load_3d(dst + hf * kHalf, w ? &mvn : &mkn, hf * 64, jb.h, jb.row0, &sm.kv_full[st]);
+            }
+          } else {
+            // 8 pages x 2 halves of 16 rows x 64 values; lane = page * 2 + half
+            const int pages = min(8, (jb.cached - t * kTile + 15) / 16);
+            const int pg = lane >> 1, hf = lane & 1;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[st], (uint32_t)(pages * 4096));
+            __syncwarp();
+            if (pg < pages) {
+              const int64_t phys = p.page_table[(size_t)jb.b * p.max_pages + t * 8 + pg];
+              int64_t row = (phys * p.Hkv + jb.h) * 16;
+              if (phys < 0 || phys >= p.n_pages) {
+                atomicOr(p.err, ODA_DEVERR_PAGE_RANGE);
+                row = p.n_pages * p.Hkv * 16;           // past the pool: the copy fills zeros
+              }
+              tma_load_2d(dst + hf * kHalf + pg * 2048, w ? &mv : &mk, hf * 64, (int32_t)row, &sm.kv_full[st]);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+    }
+    if (!ok) {   // gave up: let the copies in flight land before the CTA ends
+      const uint32_t n = 2 * gs;
+      for (uint32_t i = n >= kStages ? n - kStages : 0; i < n; ++i)
+        mbar_wait_bounded(&sm.kv_full[i % kStages], (i / kStages) & 1, kWaitNs);
+      if (jobs > 0) mbar_wait_bounded(&sm.q_full, (jobs - 1) & 1, kWaitNs);
+    }
+  } else if (warp == 8) {
+    // --------------------------------------------------------------- products
+    constexpr uint32_t kIdS = mma_idesc_bf16(128, 128, false), kIdO = mma_idesc_bf16(128, 128, true);
+    uint32_t gs = 0, jobs = 0, np[2] = {0, 0};    // tiles, jobs, weights consumed per slot
+    while (ok && walk.next(p, sm, lane, jb)) {
+      ok = mbar_wait_bounded(&sm.q_full, jobs & 1, kWaitNs);
+      ++jobs;
+      const int lag = jb.dual ? 2 : 1;
+      for (int s = 0; s < jb.total + lag && ok; ++s) {
+        const int sp = s - lag;
+        bool haveK = false, haveV = false;
+        for (int i = 0; i < 2 && ok; ++i) {
+          if (sp >= 0 && sp < jb.total && active(jb, i, sp)) {
+            // O_i += P_i V
+            const uint32_t n = 2 * (gs + sp) + 1, st = n % kStages;
+            if (!haveV) {
+              ok = mbar_wait_bounded(&sm.kv_full[st], (n / kStages) & 1, kWaitNs);
+              haveV = true;
+              const int t = kv_tile(jb, sp);
+              const int valid = TREE ? (t == jb.node_tile ? jb.len : jb.cached - t * kTile) : jb.len - t * kTile;
+              if (ok && valid < kTile) {
+                // rows behind the sequence hold another one's values or old ones: their weights
+                // are 0, and 0 * NaN must not reach the sums
+                for (int x = lane; x < (kTile - valid) * 16; x += 32) {
+                  const int r = valid + (x >> 4), ch = x & 15;
+                  *reinterpret_cast<uint4*>(skv + st * kStageBytes + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) =
+                      make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+              }
+              __syncwarp();
+            }
+            if (ok) ok = mbar_wait_bounded(&sm.p_full[i], np[i] & 1, kWaitNs);
+            ++np[i];
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t a = smem_u32(skv + st * kStageBytes);
+              const bool first = jb.dual ? sp < 2 : sp == 0;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_f16_ts(tmem + kColO + i * 128, tmem + kColS + i * 128 + k * 8,
+                           smem_desc(a + k * 2048, kHalf, 1024), kIdO, !(first && k == 0));
+              if (sp + lag >= jb.total || !active(jb, i, sp + lag)) mma_commit(&sm.o_full[i]);   // the slot's last
+            }
+            __syncwarp();
+          }
+          if (s < jb.total && active(jb, i, s)) {
+            // S_i = Q_i K^T
+            const uint32_t n = 2 * (gs + s), st = n % kStages;
+            if (!haveK) {
+              ok = mbar_wait_bounded(&sm.kv_full[st], (n / kStages) & 1, kWaitNs);
+              haveK = true;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t a = smem_u32(sq + (jb.dual ? 0 : i) * kStageBytes), bk = smem_u32(skv + st * kStageBytes);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
+                mma_f16_ss(tmem + kColS + i * 128, smem_desc(a + off, 16, 1024), smem_desc(bk + off, 16, 1024), kIdS,
+                           k > 0);
+              }
+              mma_commit(&sm.s_full[i]);
+            }
+            __syncwarp();
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          if (sp >= 0 && sp < jb.total) mma_commit(&sm.kv_empty[(2 * (gs + sp) + 1) % kStages]);
+          if (s < jb.total) mma_commit(&sm.kv_empty[(2 * (gs + s)) % kStages]);
+          if (s == jb.total - 1) mma_commit(&sm.q_empty);
+        }
+        __syncwarp();
+      }
+      gs += jb.total;
+    }
+    if (!ok) {
+      // gave up: let the products in flight (microseconds) finish before TMEM is freed
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 1000000ull) {
+      }
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---------------------------------------------------------------- weights
+    const int i = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + kColS + i * 128;
+    const uint32_t tO = tmem + lane_base + kColO + i * 128;
+    const int tok = r / p.g, hh = r - tok * p.g;
+    uint32_t ns = 0, no = 0, duals = 0;  // scores, results and joins of this slot so far
+    while (ok && walk.next(p, sm, lane, jb)) {
+      const int mine = jb.dual ? 0 : i;  // slot whose rows these are
+      const int place = jb.tok0 + mine * p.nt + tok;
+      const bool row_ok = tok < jb.n[mine];
+      uint64_t anc = 0;
+      if (TREE && row_ok && jb.first + jb.total > jb.node_tile) anc = ancestors(p.parent + jb.row0, place, p.err);
+      const int cnt = slot_steps(jb, i);
+      float m = -INFINITY, l = 0.f;
+      for (int x = 0; x < cnt && ok; ++x) {
+        const int s = jb.dual ? 2 * x + i : x;
+        const int t = kv_tile(jb, s);
+        ok = mbar_wait_bounded(&sm.s_full[i], ns & 1, kWaitNs);
+        ++ns;
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(v + 32 * q, tS + 32 * q);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) pin32(v + 32 * q);
+        // ---- mask
+        uint32_t mw[4];
+        if (TREE) {
+          if (t == jb.node_tile) {
+            mw[0] = (uint32_t)anc;
+            mw[1] = (uint32_t)(anc >> 32);
+            mw[2] = mw[3] = 0;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mw[q] = low_bits(jb.cached - t * kTile - 32 * q);
+          }
+        } else {
+          const int hi = place - t * kTile + 1;          // columns seen from the start of the tile
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            mw[q] = low_bits(hi - 32 * q);
+            if (p.local)
+              mw[q] &= ~low_bits(place - p.window + 1 - t * kTile - 32 * q) | low_bits(p.sinks - t * kTile - 32 * q);
+          }
+        }
+        if (__any_sync(0xffffffffu, (mw[0] & mw[1] & mw[2] & mw[3]) != 0xffffffffu)) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (!((mw[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;
+        }
+        // ---- reference
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool grow = top * p.c > m * p.c + kGrow;   // also the first finite value (m = -inf)
+        if (__any_sync(0xffffffffu, grow)) {
+          const float nm = fmaxf(m, top);
+          const float al = m == nm ? 1.f : exp2_approx((m - nm) * p.c);
+          m = nm;
+          l *= al;
+          if (x > 0) {
+            // these scores were issued after the slot's previous product, so that one is in O
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[32];
+              tmem_ld32(o, tO + 32 * q);
+              tmem_wait_ld();
+              pin32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+              tmem_st32(tO + 32 * q, o);
+            }
+          }
+        }
+        // ---- weights
+        const float mc = m == -INFINITY ? 0.f : m * p.c;
+        const uint64_t c2 = f32x2(p.c, p.c), mc2 = f32x2(-mc, -mc);
+        uint64_t sum2 = f32x2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t y = fma_f32x2(f32x2(__uint_as_float(v[32 * q + 2 * e]), __uint_as_float(v[32 * q + 2 * e + 1])), c2, mc2);
+            float a, b;
+            f32x2_split(y, a, b);
+            a = exp2_approx(a);
+            b = exp2_approx(b);
+            sum2 = add_f32x2(sum2, f32x2(a, b));
+            w[e] = cvt_bf16x2(a, b);
+          }
+          tmem_st16(tS + 16 * q, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[i]);
+        float a, b;
+        f32x2_split(sum2, a, b);
+        l += a + b;
+      }
+      if (!ok) break;
+      // ---- the slot's result
+      if (cnt > 0) {
+        ok = mbar_wait_bounded(&sm.o_full[i], no & 1, kWaitNs);
+        ++no;
+        if (!ok) break;
+        tc_fence_after();
+      }
+      float a0 = 1.f, a1 = 0.f;          // factors of O0 and O1
+      if (jb.dual) {
+        if (i == 1) {
+          sm.other[r] = make_float2(m, l);
+          tc_fence_before();
+          mbar_arrive(&sm.m_ready);
+          ok = mbar_wait_bounded(&sm.m_done, duals & 1, kWaitNs);
+          ++duals;
+          tc_fence_after();
+          continue;
+        }
+        ok = mbar_wait_bounded(&sm.m_ready, duals & 1, kWaitNs);
+        ++duals;
+        if (!ok) break;
+        tc_fence_after();
+        const float2 ml = sm.other[r];
+        const float nm = fmaxf(m, ml.x);
+        a0 = m == nm ? 1.f : exp2_approx((m - nm) * p.c);
+        a1 = ml.x == nm ? 1.f : exp2_approx((ml.x - nm) * p.c);
+        m = nm;
+        l = l * a0 + ml.y * a1;
+      }
+      if (cnt > 0) {
+        if (jb.direct) {
+          const float inv = l > 0.f ? __fdividef(1.f, l) : (l == 0.f ? 0.f : l);
+          a0 *= inv;
+          a1 *= inv;
+        }
+        uint4* dst = nullptr;
+        if (row_ok) {
+          if (jb.direct)
+            dst = reinterpret_cast<uint4*>(p.out + ((size_t)(jb.row0 + place) * p.Hq + jb.h * p.g + hh) * 128);
+          else
+            dst = reinterpret_cast<uint4*>(p.part_o + ((size_t)jb.part * 256 + mine * 128 + r) * 128);
+        }
+        if (row_ok && !jb.direct)
+          reinterpret_cast<float2*>(p.part_ml)[(size_t)jb.part * 256 + mine * 128 + r] = make_float2(m, l);
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[32];
+          tmem_ld32(o, tO + 32 * q);
+          tmem_wait_ld();
+          pin32(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a0);
+          if (jb.dual) {
+            uint32_t o1[32];
+            tmem_ld32(o1, tO + 128 + 32 * q);
+            tmem_wait_ld();
+            pin32(o1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(o1[e]) * a1);
+          }
+          if (dst) {
+            if (jb.direct) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint4 w;
+                w.x = cvt_bf16x2(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1]));
+                w.y = cvt_bf16x2(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3]));
+                w.z = cvt_bf16x2(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5]));
+                w.w = cvt_bf16x2(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7]));
+                dst[4 * q + e] = w;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dst[8 * q + e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+      }
+      if (jb.dual) mbar_arrive(&sm.m_done);
+    }
+  }
+  if (!ok && lane == 0) atomicOr(p.err, ODA_DEVERR_WAIT_TIMEOUT);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// Joins the partial results of the units that several CTAs shared: one warp per (node, query head).
+__global__ void __launch_bounds__(256) tree_join_kernel(const TileParams p, int grid) {
+  grid_dependency_wait();
+  const int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int64_t row = id / p.Hq;
+  const int head = (int)(id - row * p.Hq);
+  if (row >= p.n_rows) return;
+  int b = -1;                            // the sequence of this row, if it has tiles
+  for (int b0 = 0; b0 < p.n_seqs && b < 0; b0 += 32) {
+    const int x = b0 + lane;
+    const uint32_t here = __ballot_sync(0xffffffffu, x < p.n_seqs && p.cu[x] <= row && row < p.cu[x + 1] &&
+                                                         p.plan[x] != p.plan[x + 1]);
+    if (here) b = b0 + __ffs((int)here) - 1;
+  }
+  if (b < 0) return;
+  const uint32_t before = p.plan[b], W = p.plan[p.n_seqs];
+  const uint32_t share = (W + grid - 1) / grid;
+  const int len = p.cu[b + 1] - p.cu[b], node = (int)(row - p.cu[b]);
+  const uint32_t tiles = (uint32_t)((p.pos[b] - 1 + kTile - 1) / kTile + 1);
+  const uint32_t M = (uint32_t)((len + 2 * p.nt - 1) / (2 * p.nt));
+  const uint32_t h = (uint32_t)(head / p.g), hh = (uint32_t)(head % p.g);
+  const uint32_t us = before + (h * M + (uint32_t)(node / (2 * p.nt))) * tiles, ue = us + tiles;
+  const uint32_t c0 = us / share, c1 = (ue - 1) / share;
+  if (c0 == c1) return;                                  // one CTA had it all and wrote it
+  const int in = node % (2 * p.nt);
+  const int r = (in / p.nt) * 128 + (in % p.nt) * p.g + (int)hh;
+  float m = -INFINITY;
+  for (uint32_t c = c0 + lane; c <= c1; c += 32) {
+    const size_t at = (size_t)(us > c * share ? 2 * c + 1 : 2 * c) * 256 + r;
+    m = fmaxf(m, p.part_ml[2 * at]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (uint32_t c = c0; c <= c1; ++c) {
+    const size_t at = (size_t)(us > c * share ? 2 * c + 1 : 2 * c) * 256 + r;
+    const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[at];
+    const float4 o = reinterpret_cast<const float4*>(p.part_o)[at * 32 + lane];
+    const float w = ml.x == m ? 1.f : exp2_approx((ml.x - m) * p.c);
+    l += w * ml.y;
+    acc.x += w * o.x;
+    acc.y += w * o.y;
+    acc.z += w * o.z;
+    acc.w += w * o.w;
+  }
+  const float inv = __fdividef(1.f, l);
+  uint2 w;
+  w.x = cvt_bf16x2(acc.x * inv, acc.y * inv);
+  w.y = cvt_bf16x2(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2*>(p.out)[((size_t)row * p.Hq + head) * 32 + lane] = w;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+EncodeFn get_encode() {
+  static const EncodeFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<EncodeFn>(ptr);
+  }();
+  return fn;
+}
+
+oda_status encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                  const cuuint32_t* box) {
+  EncodeFn enc = get_encode();
+  if (!enc) return set_error(ODA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims,
+                         strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(ODA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return ODA_OK;
+}
+
+// Packed rows [n_rows][heads][128] with a row stride in elements: boxes of 64 values x `heads_box`
+// heads x `rows_box` rows, which land in shared memory as rows of (row, head).
+oda_status encode_rows(CUtensorMap* m, const void* ptr, int64_t n_rows, int heads, int64_t stride,
+                       int heads_box, int rows_box) {
+  const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)n_rows};
+  const cuuint64_t st[2] = {256, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)heads_box, (cuuint32_t)rows_box};
+  return encode(m, ptr, 3, dims, st, box);
+}
+
+bool aligned16(const void* a) { return (reinterpret_cast<uintptr_t>(a) & 15) == 0; }
+
+}  // namespace
+
+size_t tile_part_rows(int n_sms) { return (size_t)2 * n_sms * 256; }
+
+oda_status prepare_tile_attention() {
+  // the kernel moves registers between its warpgroups, 208 + 208 + 88 of them a thread: the launch
+  // has to bring exactly as many
+  const void* f[2] = {reinterpret_cast<const void*>(tile_attention_kernel<false>),
+                      reinterpret_cast<const void*>(tile_attention_kernel<true>)};
+  for (const void* k : f) {
+    cudaFuncAttributes fa;
+    const oda_status a = check_cuda(cudaFuncGetAttributes(&fa, k), "cudaFuncGetAttributes(tile attention)");
+    if (a != ODA_OK) return a;
+    if (fa.numRegs * 3 < 208 + 208 + 88)
+      return set_error(ODA_ERR_UNSUPPORTED, "tile attention: built with %d registers a thread", fa.numRegs);
+  }
+  oda_status st = check_cuda(cudaFuncSetAttribute(tile_attention_kernel<false>,
+                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kDynBytes),
+                             "cudaFuncSetAttribute(prompt attention)");
+  if (st == ODA_OK)
+    st = check_cuda(cudaFuncSetAttribute(tile_attention_kernel<true>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kDynBytes),
+                    "cudaFuncSetAttribute(tree attention)");
+  return st;
+}
+
+oda_status launch_prompt(oda_ctx* ctx, int n_seqs, int64_t n_rows, const int32_t* cu_rows, const void* q,
+                         const void* k, const void* v, int64_t q_stride, int64_t kv_stride, void* out, int local,
+                         cudaStream_t stream) {
+  const oda_config& cf = ctx->cfg;
+  if (!cu_rows || !q || !k || !v || !out) return set_error(ODA_ERR_INVALID_ARG, "prompt: null pointer argument");
+  if (n_seqs < 1 || n_seqs > ODA_MAX_BATCH)
+    return set_error(ODA_ERR_INVALID_ARG, "prompt: n_seqs must be 1..%d", ODA_MAX_BATCH);
+  if (n_rows < 1 || n_rows * (int64_t)cf.n_q_heads > INT32_MAX)
+    return set_error(ODA_ERR_INVALID_ARG, "prompt: n_rows out of range (%lld)", (long long)n_rows);
+  if (q_stride < (int64_t)cf.n_q_heads * 128 || kv_stride < (int64_t)cf.n_kv_heads * 128 || (q_stride & 7) ||
+      (kv_stride & 7) || q_stride > (int64_t(1) << 32) || kv_stride > (int64_t(1) << 32))
+    return set_error(ODA_ERR_INVALID_ARG, "prompt: row strides must cover the heads and be multiples of 8");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
+    return set_error(ODA_ERR_INVALID_ARG, "prompt: q, k, v and out must be 16-byte aligned");
+  ctx->prev_attention = false;
+  TileParams p = {};
+  p.cu = cu_rows;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.err = ctx->err;
+  p.n_rows = n_rows;
+  p.n_seqs = n_seqs;
+  p.Hq = cf.n_q_heads;
+  p.Hkv = cf.n_kv_heads;
+  p.g = ctx->g;
+  p.nt = kTile / ctx->g;
+  p.local = local;
+  p.sinks = cf.sinks;
+  p.window = cf.window;
+  p.c = (float)(1.4426950408889634 / std::sqrt(128.0));
+  CUtensorMap mq, mk, mv;
+  oda_status st = encode_rows(&mq, q, n_rows, cf.n_q_heads, q_stride, p.g, p.nt);
+  if (st == ODA_OK) st = encode_rows(&mk, k, n_rows, cf.n_kv_heads, kv_stride, 1, kTile);
+  if (st == ODA_OK) st = encode_rows(&mv, v, n_rows, cf.n_kv_heads, kv_stride, 1, kTile);
+  if (st != ODA_OK) return st;
+  const int64_t most = (n_rows / (2 * p.nt) + n_seqs) * cf.n_kv_heads;
+  const int grid = (int)std::min<int64_t>(ctx->n_sms, most);
+  tile_attention_kernel<false><<<grid, kThreads, kDynBytes, stream>>>(mq, mk, mv, mk, mv, p);
+  return check_cuda(cudaGetLastError(), "prompt attention launch");
+}
+
+oda_status launch_tree(oda_ctx* ctx, const oda_kv_layer* layer, const int32_t* page_table, const int32_t* pos,
+                       const int32_t* flag, int64_t n_rows, const int32_t* cu_rows, const int32_t* parent,
+                       const void* q, const void* k_new, const void* v_new, void* out, cudaStream_t stream) {
+  const oda_config& cf = ctx->cfg;
+  if (!layer || !layer->k || !layer->v || !page_table || !pos || !cu_rows || !parent || !q || !k_new || !v_new || !out)
+    return set_error(ODA_ERR_INVALID_ARG, "tree: null pointer argument");
+  if (layer->n_pages <= 0 || (layer->n_pages + 1) * (int64_t)cf.n_kv_heads * 16 > INT32_MAX)
+    return set_error(ODA_ERR_INVALID_ARG, "tree: n_pages out of range (%lld)", (long long)layer->n_pages);
+  if (n_rows < 1 || n_rows > (int64_t)cf.batch * ODA_MAX_TREE)
+    return set_error(ODA_ERR_INVALID_ARG, "tree: n_rows must be 1..batch * %d", ODA_MAX_TREE);
+  if (!aligned16(layer->k) || !aligned16(layer->v) || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) ||
+      !aligned16(out))
+    return set_error(ODA_ERR_INVALID_ARG, "tree: pools, q, k_new, v_new and out must be 16-byte aligned");
+  TileParams p = {};
+  p.nt = kTile / ctx->g;
+  const int64_t units = (ODA_MAX_TREE + 2 * p.nt - 1) / (2 * p.nt);
+  if ((int64_t)cf.batch * cf.n_kv_heads * units * ((cf.max_pages + 7) / 8 + 1) > (int64_t)INT32_MAX)
+    return set_error(ODA_ERR_UNSUPPORTED, "tree: batch * KV heads * max_pages beyond the tile count");
+  ctx->prev_attention = false;
+  p.cu = cu_rows;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.err = ctx->err;
+  p.n_rows = n_rows;
+  p.n_seqs = cf.batch;
+  p.Hq = cf.n_q_heads;
+  p.Hkv = cf.n_kv_heads;
+  p.g = ctx->g;
+  p.c = (float)(1.4426950408889634 / std::sqrt(128.0));
+  p.page_table = page_table;
+  p.pos = pos;
+  p.flag = flag;
+  p.parent = parent;
+  p.n_pages = layer->n_pages;
+  p.max_pages = cf.max_pages;
+  p.part_o = ctx->tile_part_o;
+  p.part_ml = ctx->tile_part_ml;
+  p.plan = ctx->tile_plan;
+  CUtensorMap mq, mk, mv, mkn, mvn;
+  const cuuint64_t dims[2] = {128, (cuuint64_t)layer->n_pages * cf.n_kv_heads * 16};
+  const cuuint64_t str[1] = {256};
+  const cuuint32_t box[2] = {64, 16};
+  oda_status st = encode(&mk, layer->k, 2, dims, str, box);
+  if (st == ODA_OK) st = encode(&mv, layer->v, 2, dims, str, box);
+  if (st == ODA_OK) st = encode_rows(&mq, q, n_rows, cf.n_q_heads, (int64_t)cf.n_q_heads * 128, p.g, p.nt);
+  if (st == ODA_OK) st = encode_rows(&mkn, k_new, n_rows, cf.n_kv_heads, (int64_t)cf.n_kv_heads * 128, 1, ODA_MAX_TREE);
+  if (st == ODA_OK) st = encode_rows(&mvn, v_new, n_rows, cf.n_kv_heads, (int64_t)cf.n_kv_heads * 128, 1, ODA_MAX_TREE);
+  if (st != ODA_OK) return st;
+  const int grid = ctx->n_sms;
+  tile_attention_kernel<true><<<grid, kThreads, kDynBytes, stream>>>(mq, mk, mv, mkn, mvn, p);
+  st = check_cuda(cudaGetLastError(), "tree attention launch");
+  if (st != ODA_OK) return st;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)((n_rows * cf.n_q_heads + 7) / 8));
+  lc.blockDim = dim3(256);
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return check_cuda(cudaLaunchKernelEx(&lc, tree_join_kernel, p, grid), "tree join launch");
+}
+
+}  // namespace oda

@@ -299,6 +299,133 @@ def oda_glue_gdn(ctx, st: OdaState, layer: int, c, v, alpha, beta, taps, flag, o
                                    _p(beta), _p(taps), _p(flag), _p(o), _s(stream)))
 
 
+# ------------------------------------------------- prompts, drafted trees, append, sampling
+def _want(name, t, dtypes, shape=None):
+    """A CUDA tensor of one of the element types and the given contiguous shape (None: any length)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if shape is not None:
+        if t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape)):
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+_BF16 = (torch.bfloat16, torch.int16)
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+
+
+def _prompt_rows(name, t, heads):
+    """Row stride of packed rows [n, heads, 128] whose heads are contiguous inside a row."""
+    _want(name, t, _BF16)
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128 or t.stride(2) != 1 or \
+            (heads > 1 and t.stride(1) != 128):
+        raise ValueError(f"{name}: expected rows [n, {heads}, 128] with contiguous heads")
+    return t.stride(0) if t.shape[0] > 1 else max(heads * 128, t.stride(0))
+
+
+def _attend_prompt(fn, ctx, cu_rows, q, k, v, out, stream):
+    Hq, Hkv = ctx.cfg.n_q_heads, ctx.cfg.n_kv_heads
+    _want("cu_rows", cu_rows, _I32, (None,))
+    qs, ks, vs = _prompt_rows("q", q, Hq), _prompt_rows("k", k, Hkv), _prompt_rows("v", v, Hkv)
+    n = int(q.shape[0])
+    if k.shape[0] != n or v.shape[0] != n:
+        raise ValueError("q, k and v must have the same number of rows")
+    if ks != vs:
+        raise ValueError("k and v must have the same row stride")
+    _want("out", out, _BF16, (n, Hq, 128))
+    check(fn(ctx.handle, int(cu_rows.shape[0]) - 1, n, _p(cu_rows), _p(q), _p(k), _p(v), qs, ks, _p(out),
+             _s(stream)))
+
+
+def oda_attend_full_prompt(ctx, cu_rows, q, k, v, out, stream=None):
+    """Causal attention over packed prompts, S^F: q [n, Hq, 128], k, v [n, Hkv, 128] (rows may be
+    strided), out [n, Hq, 128], all bf16; cu_rows int32 [n_seqs + 1]."""
+    _attend_prompt(_lib.load().oda_attend_full_prompt, ctx, cu_rows, q, k, v, out, stream)
+
+
+def oda_attend_local_prompt(ctx, cu_rows, q, k, v, out, stream=None):
+    """The same over the local set S^L of every position."""
+    _attend_prompt(_lib.load().oda_attend_local_prompt, ctx, cu_rows, q, k, v, out, stream)
+
+
+def oda_attend_full_tree(ctx, layer: OdaKVLayer, page_table, pos, flag, cu_rows, parent, q, k_new, v_new, out,
+                         stream=None):
+    """A tree of drafted tokens per sequence over the paged cache; flag None: every sequence."""
+    c = ctx.cfg
+    n = int(q.shape[0])
+    _want("page_table", page_table, _I32, (c.batch, c.max_pages))
+    _want("pos", pos, _I32, (c.batch,))
+    if flag is not None:
+        _want("flag", flag, _I32, (c.batch,))
+    _want("cu_rows", cu_rows, _I32, (c.batch + 1,))
+    _want("parent", parent, _I32, (n,))
+    _want("q", q, _BF16, (n, c.n_q_heads, 128))
+    _want("k_new", k_new, _BF16, (n, c.n_kv_heads, 128))
+    _want("v_new", v_new, _BF16, (n, c.n_kv_heads, 128))
+    _want("out", out, _BF16, (n, c.n_q_heads, 128))
+    check(_lib.load().oda_attend_full_tree(ctx.handle, ctypes.byref(layer), _p(page_table), _p(pos), _p(flag), n,
+                                           _p(cu_rows), _p(parent), _p(q), _p(k_new), _p(v_new), _p(out),
+                                           _s(stream)))
+
+
+def _append(fn, cls, ctx, layers, page_table, pos, cu_rows, rows, k_stage, v_stage, h_stage, h_prev, pos_next,
+            stream):
+    c = ctx.cfg
+    arr = (cls * len(layers))(*layers)
+    _want("page_table", page_table, _I32, (c.batch, c.max_pages))
+    _want("pos", pos, _I32, (c.batch,))
+    _want("cu_rows", cu_rows, _I32, (c.batch + 1,))
+    _want("k_stage", k_stage, _BF16, (len(layers), None, c.n_kv_heads, 128))
+    n_stage = int(k_stage.shape[1])
+    _want("v_stage", v_stage, _BF16, (len(layers), n_stage, c.n_kv_heads, 128))
+    if rows is not None:
+        _want("rows", rows, _I32, (None,))
+    if h_stage is not None:
+        _want("h_stage", h_stage, _F32, (n_stage, c.head_in_dim))
+    if h_prev is not None:
+        _want("h_prev", h_prev, _F32, (c.batch, c.head_in_dim))
+    if pos_next is not None:
+        _want("pos_next", pos_next, _I32, (c.batch,))
+    n_rows = n_stage if rows is None else int(rows.shape[0])
+    check(fn(ctx.handle, arr, len(layers), _p(page_table), _p(pos), n_rows, n_stage, _p(cu_rows), _p(rows),
+             _p(k_stage), _p(v_stage), _p(h_stage), _p(h_prev), _p(pos_next), _s(stream)))
+
+
+def oda_append(ctx, layers: Sequence[OdaKVLayer], page_table, pos, cu_rows, rows, k_stage, v_stage, h_stage=None,
+               h_prev=None, pos_next=None, stream=None):
+    """Rows of k_stage, v_stage (bf16 [n_layers, n_stage, Hkv, 128]) to positions pos[b].. of the pages;
+    rows (int32, packed as cu_rows says) picks them, None takes them in order."""
+    _append(_lib.load().oda_append, OdaKVLayer, ctx, layers, page_table, pos, cu_rows, rows, k_stage, v_stage,
+            h_stage, h_prev, pos_next, stream)
+
+
+def oda_append_fp8(ctx, layers: Sequence[OdaKV8Layer], page_table, pos, cu_rows, rows, k_stage, v_stage,
+                   h_stage=None, h_prev=None, pos_next=None, stream=None):
+    """The same into fp8 pages."""
+    _append(_lib.load().oda_append_fp8, OdaKV8Layer, ctx, layers, page_table, pos, cu_rows, rows, k_stage, v_stage,
+            h_stage, h_prev, pos_next, stream)
+
+
+def oda_sample(ctx, logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, prob=None, stream=None):
+    """token[r] (int32) of each row of fp32 logits [n, vocab] (rows may be strided) from u[r] in [0, 1);
+    the settings are device tensors [n] or None (off)."""
+    _want("logits", logits, _F32)
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: expected [n, vocab] with contiguous rows")
+    n, vocab = int(logits.shape[0]), int(logits.shape[1])
+    for name, t, dt in (("u", u, _F32), ("token", token, _I32), ("temperature", temperature, _F32),
+                        ("top_k", top_k, _I32), ("top_p", top_p, _F32), ("min_p", min_p, _F32), ("prob", prob, _F32)):
+        if t is not None or name in ("u", "token"):
+            _want(name, t, dt, (n,))
+    stride = logits.stride(0) if n > 1 else max(vocab, logits.stride(0))
+    check(_lib.load().oda_sample(ctx.handle, n, vocab, stride, _p(logits), _p(temperature), _p(top_k), _p(top_p),
+                                 _p(min_p), _p(u), _p(token), _p(prob), _s(stream)))
+
+
 # ------------------------------------------------------------------ synthetic backbone
 def bb_layer(attn_norm, w_qkv, w_o, mlp_norm, w_gate, w_up, w_down) -> OdaBBLayer:
     """Layer descriptor from device tensors (norm weights fp32 [D]; projections bf16 or int16
