@@ -16,7 +16,8 @@
 //   warps 0-3, 4-7: one thread per row of slot 0 / 1: scores from TMEM, weights back to TMEM as bf16
 //   warp 8:         issues the products S = Q K^T and O += P V (M = N = 128, 16-deep steps)
 //   warp 9:         brings Q, K and V by TMA (5 stages of 32 KB for K and V tiles)
-//   warps 10, 11:   idle (they complete the warpgroup whose registers go to the other two)
+//   warp 10:        plans the CTA's units of work, two ahead
+//   warp 11:        idle (it completes the warpgroup whose registers go to the other two)
 //
 // TMEM: S0 | S1 | O0 | O1, 128 columns each; P_i overwrites the first 64 columns of S_i.
 // Every wait is bounded; a wait that gives up sets ODA_DEVERR_WAIT_TIMEOUT and ends the CTA.
@@ -35,10 +36,15 @@ constexpr int kTile = 128;              // query rows of a slot; positions of a 
 constexpr int kStages = 5;
 constexpr int kStageBytes = kTile * 256;
 constexpr int kHalf = kTile * 128;      // bytes of one 64-value half of a tile
-constexpr int kThreads = 384;           // 168 registers a thread at launch, then 208 / 208 / 88 by warpgroup
+constexpr int kThreads = 384;           // 168 registers a thread at launch, then 200, 200 and 104 by warpgroup
+constexpr int kRegs = 168, kRegsRow = 200, kRegsOther = 104;
+static_assert(2 * kRegsRow + kRegsOther == 3 * kRegs, "the split has to add up to the launch");
+constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpPlan = 10;
+constexpr int kAhead = 2;               // units planned ahead
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 8.0f;           // log2 of the growth that moves a row's reference
 constexpr uint32_t kColS = 0, kColO = 256;
+constexpr int kPoly = 4;                  // one pair of weights in 4 is made on the FMA pipe
 
 struct TileParams {
   const int32_t* cu;
@@ -60,28 +66,15 @@ struct TileParams {
   uint32_t* plan;                       // [n_seqs + 1] tiles before each sequence
 };
 
-struct Smem {
-  uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t m_ready, m_done;
-  float2 other[kTile];                  // slot 1's reference and sum where the slots are joined
-  uint32_t tmem;
-  uint32_t pref[ODA_MAX_BATCH + 1];     // prompt: blocks of each sequence; tree: tiles before it
-};
-constexpr int kTileBytes = (2 + kStages) * kStageBytes;   // Q slots, then K and V stages
-constexpr int kDynBytes = kTileBytes + sizeof(Smem);
-static_assert(kDynBytes <= 227 * 1024, "shared memory of a CTA");
-
 // A CTA's unit of work: up to two slots of one KV head against a run of KV tiles.
 struct Job {
   int b, h;            // sequence, KV head
   int row0;            // packed row of the sequence's first token or node
   int len;             // its tokens or nodes
   int tok0;            // first token of slot 0
-  int n[2];            // valid tokens of each slot
+  int n0, n1;          // valid tokens of each slot
   int first, sink;     // KV tile of step s: s == 0 && sink ? 0 : first + s - sink
-  int steps[2];        // steps of each slot (dual: of the job)
+  int steps0, steps1;  // steps of each slot (dual: of the job)
   int total;
   int dual;
   int cached;          // tree: cached positions; prompt: unused
@@ -89,9 +82,23 @@ struct Job {
   int direct;          // result complete: write out, else a partial
   int part;            // partial slot
 };
+struct Smem {
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_ready[2][2], o_full[2];
+  uint64_t m_ready, m_done;
+  uint64_t job_full[kAhead], job_empty[kAhead];
+  float2 other[kTile];                  // slot 1's reference and sum where the slots are joined
+  Job jobs[kAhead];
+  uint32_t tmem;
+  uint32_t pref[ODA_MAX_BATCH + 1];     // prompt: blocks of each sequence; tree: tiles before it
+};
+constexpr int kTileBytes = (2 + kStages) * kStageBytes;   // Q slots, then K and V stages
+constexpr int kDynBytes = kTileBytes + sizeof(Smem);
+static_assert(kDynBytes <= 227 * 1024, "shared memory of a CTA");
+
 __device__ __forceinline__ int kv_tile(const Job& j, int s) { return (j.sink && s == 0) ? 0 : j.first + s - j.sink; }
-__device__ __forceinline__ bool active(const Job& j, int i, int s) { return j.dual ? (s & 1) == i : s < j.steps[i]; }
-__device__ __forceinline__ int slot_steps(const Job& j, int i) { return j.dual ? (j.total + 1 - i) >> 1 : j.steps[i]; }
+__device__ __forceinline__ int slot_steps(const Job& j, int i) { return j.dual ? (j.total + 1 - i) >> 1 : i ? j.steps1 : j.steps0; }
 
 __device__ __forceinline__ int seq_len(const TileParams& p, int b, int most, bool report) {
   const int a = p.cu[b], e = p.cu[b + 1];
@@ -131,8 +138,9 @@ __device__ __forceinline__ bool prompt_job(const TileParams& p, const Smem& sm, 
   for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
     const uint32_t here = __ballot_sync(0xffffffffu, b0 + lane < p.n_seqs && sm.pref[b0 + lane] > lo);
     const uint32_t cnt = __popc(here);
-    if (k < cnt) {
-      b = b0 + (int)__fns(here, 0, (int)k + 1);
+    if (k < cnt) {                       // the k-th of them
+      const bool it = ((here >> lane) & 1u) && __popc(here & ((1u << lane) - 1u)) == (int)k;
+      b = b0 + __ffs((int)__ballot_sync(0xffffffffu, it)) - 1;
       break;
     }
     k -= cnt;
@@ -142,15 +150,15 @@ __device__ __forceinline__ bool prompt_job(const TileParams& p, const Smem& sm, 
   jb.row0 = p.cu[b];
   jb.len = p.cu[b + 1] - jb.row0;
   jb.tok0 = (int)lo * 2 * p.nt;
-  jb.n[0] = min(p.nt, jb.len - jb.tok0);
-  jb.n[1] = max(0, min(p.nt, jb.len - jb.tok0 - p.nt));
+  jb.n0 = min(p.nt, jb.len - jb.tok0);
+  jb.n1 = max(0, min(p.nt, jb.len - jb.tok0 - p.nt));
   jb.first = 0;
   if (p.local && jb.tok0 >= p.window) jb.first = (jb.tok0 - p.window + 1) / kTile;
   jb.sink = (p.local && p.sinks > 0 && jb.first > 0) ? 1 : 0;
-  jb.steps[0] = (jb.tok0 + jb.n[0] - 1) / kTile - jb.first + 1 + jb.sink;
-  jb.steps[1] = jb.n[1] > 0 ? (jb.tok0 + p.nt + jb.n[1] - 1) / kTile - jb.first + 1 + jb.sink : 0;
-  jb.total = max(jb.steps[0], jb.steps[1]);
-  jb.dual = jb.n[1] == 0 && jb.total > 1;
+  jb.steps0 = (jb.tok0 + jb.n0 - 1) / kTile - jb.first + 1 + jb.sink;
+  jb.steps1 = jb.n1 > 0 ? (jb.tok0 + p.nt + jb.n1 - 1) / kTile - jb.first + 1 + jb.sink : 0;
+  jb.total = max(jb.steps0, jb.steps1);
+  jb.dual = jb.n1 == 0 && jb.total > 1;
   jb.node_tile = -1;
   jb.cached = 0;
   jb.direct = 1;
@@ -182,14 +190,14 @@ __device__ __forceinline__ bool tree_job(const TileParams& p, const Smem& sm, ui
   const uint32_t j1 = min(tiles, j0 + (end - at));
   jb.h = (int)(u / M);
   jb.tok0 = (int)(u % M) * 2 * p.nt;
-  jb.n[0] = min(p.nt, jb.len - jb.tok0);
-  jb.n[1] = max(0, min(p.nt, jb.len - jb.tok0 - p.nt));
+  jb.n0 = min(p.nt, jb.len - jb.tok0);
+  jb.n1 = max(0, min(p.nt, jb.len - jb.tok0 - p.nt));
   jb.first = (int)j0;
   jb.sink = 0;
   jb.total = (int)(j1 - j0);
-  jb.steps[0] = jb.total;
-  jb.steps[1] = jb.n[1] > 0 ? jb.total : 0;
-  jb.dual = jb.n[1] == 0 && jb.total > 1;
+  jb.steps0 = jb.total;
+  jb.steps1 = jb.n1 > 0 ? jb.total : 0;
+  jb.dual = jb.n1 == 0 && jb.total > 1;
   jb.node_tile = (int)tiles - 1;
   jb.direct = j0 == 0 && j1 == tiles;
   jb.part = 2 * (int)blockIdx.x + (at == begin ? 0 : 1);
@@ -200,7 +208,7 @@ __device__ __forceinline__ bool tree_job(const TileParams& p, const Smem& sm, ui
 // Walks the CTA's jobs; every warp walks them by itself.
 template <bool TREE>
 struct Walk {
-  uint32_t at, begin, end, stride;
+  uint32_t at, begin, end, turn;
   __device__ Walk(const TileParams& p, const Smem& sm) {
     if (TREE) {
       const uint32_t W = sm.pref[p.n_seqs];
@@ -208,18 +216,18 @@ struct Walk {
       begin = min(W, share * blockIdx.x);
       end = min(W, begin + share);
       at = begin;
-      stride = 0;
     } else {
-      at = blockIdx.x;
-      begin = end = 0;
-      stride = gridDim.x;
+      at = begin = end = 0;
     }
+    turn = 0;
   }
   __device__ bool next(const TileParams& p, const Smem& sm, int lane, Job& j) {
     if (TREE) return tree_job(p, sm, at, begin, end, j);
-    if (!prompt_job(p, sm, at, lane, j)) return false;
-    at += stride;
-    return true;
+    // the units fall in cost: odd turns go the other way round the CTAs, so that none gets the
+    // longest of every turn
+    const uint32_t id = turn * gridDim.x + ((turn & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    ++turn;
+    return prompt_job(p, sm, id, lane, j);
   }
 };
 
@@ -242,9 +250,90 @@ __device__ __forceinline__ uint64_t ancestors(const int32_t* parent, int i, int3
   return m;
 }
 
+__device__ __forceinline__ void pin16(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+// Keeps what reads registers loaded from TMEM behind the wait for that load.
 __device__ __forceinline__ void pin32(uint32_t* r) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// 2^x of a pair on the FMA pipe: x = n + f with n whole and |f| <= 1/2, 2^f by the cubic of least
+// relative error on that range (7.5e-5, fitted by reweighted least squares; the weights are then
+// rounded to bf16, 3.9e-3), n added to the exponent.  x is held at -125 from below.
+__device__ __forceinline__ void exp2_pair(uint64_t x2, float& a, float& b) {
+  f32x2_split(x2, a, b);
+  x2 = f32x2(fmaxf(a, -125.f), fmaxf(b, -125.f));
+  const float kRound = 12582912.f;       // 1.5 * 2^23: adding it rounds to a whole number
+  const uint64_t t2 = add_f32x2(x2, f32x2(kRound, kRound));
+  const uint64_t n2 = add_f32x2(t2, f32x2(-kRound, -kRound));
+  const uint64_t f2 = fma_f32x2(n2, f32x2(-1.f, -1.f), x2);
+  uint64_t y2 = fma_f32x2(f2, f32x2(0.05517132f, 0.05517132f), f32x2(0.24261054f, 0.24261054f));
+  y2 = fma_f32x2(y2, f2, f32x2(0.69326099f, 0.69326099f));
+  y2 = fma_f32x2(y2, f2, f32x2(0.99992811f, 0.99992811f));
+  float ta, tb;
+  f32x2_split(t2, ta, tb);
+  f32x2_split(y2, a, b);
+  a = __uint_as_float(__float_as_uint(a) + (__float_as_uint(ta) << 23));
+  b = __uint_as_float(__float_as_uint(b) + (__float_as_uint(tb) << 23));
+}
+
+// Weights 2^(c v - mc) of 32 columns as bf16 pairs, and their sums (unrounded) added to s0, s1.  The
+// exponential unit makes 16 a clock and SM, 2048 clocks for the two slots' tiles, as long as the tile's
+// products: one pair in kPoly goes to the FMA pipe.
+__device__ __forceinline__ void weights(uint32_t* w, const uint32_t* v, uint64_t c2, uint64_t mc2, uint64_t& s0, uint64_t& s1) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const uint64_t x2 = fma_f32x2(f32x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), c2, mc2);
+    float a, b;
+    if (e % kPoly == kPoly - 1) {
+      exp2_pair(x2, a, b);
+    } else {
+      f32x2_split(x2, a, b);
+      a = exp2_approx(a);
+      b = exp2_approx(b);
+    }
+    if (e & 1) s1 = add_f32x2(s1, f32x2(a, b));
+    else s0 = add_f32x2(s0, f32x2(a, b));
+    w[e] = cvt_bf16x2(a, b);
+  }
+}
+
+// Masked ones of 32 scores to -inf.
+__device__ __forceinline__ void mask32(uint32_t* v, uint32_t seen) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!((seen >> e) & 1u)) v[e] = 0xff800000u;
+}
+
+// Writes one line of N 16-byte chunks (N = 4 or 8; 4 N registers) per lane, line number `at` of dst (< 0:
+// none), N lanes to a line: an N x N transpose of chunks among each N lanes, then 32 / N whole lines a
+// store.  A lane writing its own line would touch 32 lines in every store.
+template <int N>
+__device__ __forceinline__ void store_lines(uint32_t* v, uint4* dst, int64_t at, int lane) {
+#pragma unroll
+  for (int bit = 1; bit < N; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      if (c & bit) continue;             // chunks c and c | bit: one of them goes to the partner lane
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t give = up ? v[4 * c + w] : v[4 * (c | bit) + w];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, bit);
+        if (up) v[4 * c + w] = got;
+        else v[4 * (c | bit) + w] = got;
+      }
+    }
+  }
+  // now chunk j of this lane is chunk (lane mod N) of the line of the j-th of its N lanes
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int64_t to = __shfl_sync(0xffffffffu, at, (lane & ~(N - 1)) + j);
+    if (to >= 0) dst[to * N + (lane & (N - 1))] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  }
 }
 
 template <bool TREE>
@@ -267,17 +356,22 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     mbar_init(&sm.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], kTile);
+      mbar_init(&sm.p_ready[i][0], 4);
+      mbar_init(&sm.p_ready[i][1], 4);
       mbar_init(&sm.o_full[i], 1);
     }
-    mbar_init(&sm.m_ready, kTile);
-    mbar_init(&sm.m_done, kTile);
+    mbar_init(&sm.m_ready, 4);
+    mbar_init(&sm.m_done, 4);
+    for (int i = 0; i < kAhead; ++i) {
+      mbar_init(&sm.job_full[i], 1);
+      mbar_init(&sm.job_empty[i], 10);
+    }
     fence_mbar_init();
   }
-  if (warp == 8) tmem_alloc(&sm.tmem, 512);
+  if (warp == kWarpMma) tmem_alloc(&sm.tmem, 512);
   if (TREE) {
     // tiles before each sequence: one warp, 32 sequences at a time
-    if (warp == 9) {
+    if (warp == kWarpLoad) {
       uint32_t run = 0;
       for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
         const int b = b0 + lane;
@@ -312,21 +406,45 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  Walk<TREE> walk(p, sm);
-  Job jb;
   bool ok = true;
+  // Every role walks the planned units: waits for one, reads it where it lies, gives it back.
+  uint32_t turn = 0;
+  auto next_job = [&]() {                // false at the end, or where the wait gave up (ok)
+    if (ok) ok = mbar_wait_bounded(&sm.job_full[turn % kAhead], (turn / kAhead) & 1, kWaitNs);
+    return ok && sm.jobs[turn % kAhead].total > 0;
+  };
+  auto done_job = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.job_empty[turn % kAhead]);
+    ++turn;
+  };
 
-  // the registers of the launch, 128 x (168 x 3), split 128 x (208 + 208 + 88)
-  if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 9) {
+  if (warp >= kWarpMma) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+  if (warp == kWarpPlan) {
+    Walk<TREE> walk(p, sm);
+    Job jb;
+    for (uint32_t n = 0; ok; ++n) {
+      const bool more = walk.next(p, sm, lane, jb);
+      if (!more) jb.total = 0;
+      const uint32_t at = n % kAhead;
+      if (n >= kAhead) ok = mbar_wait_bounded(&sm.job_empty[at], (n / kAhead - 1) & 1, kWaitNs);
+      if (ok && lane == 0) {
+        sm.jobs[at] = jb;
+        mbar_arrive(&sm.job_full[at]);
+      }
+      __syncwarp();
+      if (!more) break;
+    }
+  } else if (warp == kWarpLoad) {
     // ------------------------------------------------------------------ loads
     uint32_t gs = 0, jobs = 0;           // KV tiles (K, V counted apart: 2 gs) and jobs so far
-    while (ok && walk.next(p, sm, lane, jb)) {
+    while (next_job()) {
+      const Job& jb = sm.jobs[turn % kAhead];
       if (jobs > 0) ok = mbar_wait_bounded(&sm.q_empty, (jobs - 1) & 1, kWaitNs);
       if (!ok) break;
       if (lane == 0) {
-        const int slots = jb.n[1] > 0 ? 2 : 1;
+        const int slots = jb.n1 > 0 ? 2 : 1;
         mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(slots * 2 * 128 * p.g * p.nt));
         for (int i = 0; i < slots; ++i)
           for (int hf = 0; hf < 2; ++hf)
@@ -374,6 +492,7 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         }
         if (!ok) break;
       }
+      done_job();
     }
     if (!ok) {   // gave up: let the copies in flight land before the CTA ends
       const uint32_t n = 2 * gs;
@@ -381,85 +500,126 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         mbar_wait_bounded(&sm.kv_full[i % kStages], (i / kStages) & 1, kWaitNs);
       if (jobs > 0) mbar_wait_bounded(&sm.q_full, (jobs - 1) & 1, kWaitNs);
     }
-  } else if (warp == 8) {
+  } else if (warp == kWarpMma) {
     // --------------------------------------------------------------- products
-    constexpr uint32_t kIdS = mma_idesc_bf16(128, 128, false), kIdO = mma_idesc_bf16(128, 128, true);
-    uint32_t gs = 0, jobs = 0, np[2] = {0, 0};    // tiles, jobs, weights consumed per slot
-    while (ok && walk.next(p, sm, lane, jb)) {
-      ok = mbar_wait_bounded(&sm.q_full, jobs & 1, kWaitNs);
-      ++jobs;
-      const int lag = jb.dual ? 2 : 1;
-      for (int s = 0; s < jb.total + lag && ok; ++s) {
-        const int sp = s - lag;
-        bool haveK = false, haveV = false;
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (sp >= 0 && sp < jb.total && active(jb, i, sp)) {
-            // O_i += P_i V
-            const uint32_t n = 2 * (gs + sp) + 1, st = n % kStages;
-            if (!haveV) {
-              ok = mbar_wait_bounded(&sm.kv_full[st], (n / kStages) & 1, kWaitNs);
-              haveV = true;
-              const int t = kv_tile(jb, sp);
-              const int valid = TREE ? (t == jb.node_tile ? jb.len : jb.cached - t * kTile) : jb.len - t * kTile;
-              if (ok && valid < kTile) {
-                // rows behind the sequence hold another one's values or old ones: their weights
-                // are 0, and 0 * NaN must not reach the sums
-                for (int x = lane; x < (kTile - valid) * 16; x += 32) {
-                  const int r = valid + (x >> 4), ch = x & 15;
-                  *reinterpret_cast<uint4*>(skv + st * kStageBytes + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) =
-                      make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-              }
-              __syncwarp();
-            }
-            if (ok) ok = mbar_wait_bounded(&sm.p_full[i], np[i] & 1, kWaitNs);
-            ++np[i];
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-              const uint32_t a = smem_u32(skv + st * kStageBytes);
-              const bool first = jb.dual ? sp < 2 : sp == 0;
+    // One thread for both slots in turn, which keeps them half a period apart: with a warp for each
+    // the slots fall into step, and the tensor cores idle while both make weights.  What it runs between
+    // two products lies on the path from weights to scores, at some 8 clocks an instruction: one
+    // thread alone (no votes), running stage and phase numbers, descriptors made once.
+    if (elect_one()) {
+      constexpr uint32_t kIdS = mma_idesc_bf16(128, 128, false), kIdO = mma_idesc_bf16(128, 128, true);
+      const uint64_t dq = smem_desc(smem_u32(sq), 16, 1024), dk = smem_desc(smem_u32(skv), 16, 1024);
+      const uint64_t dv = smem_desc(smem_u32(skv), kHalf, 1024);
+      constexpr uint32_t kStep = kStageBytes >> 4;  // of a descriptor's address
+      uint32_t ks = 0, kp = 0, vs = 1, vp = 0;      // stage and phase of the next K and V tile
+      uint32_t np0 = 0, np1 = 0, jobs = 0;          // parity of each slot's weights consumed; of the jobs
+      // O_i += P_i V: the first 64 weights of every row, then the others; nk = 16-row steps of the tile
+      auto pv = [&](int i, uint32_t& np, bool acc, int nk) {
+        const uint32_t tS = tmem + kColS + i * 128, tO = tmem + kColO + i * 128;
+        const uint64_t bv = dv + vs * kStep;
+        ok = mbar_wait_bounded(&sm.p_ready[i][0], np, kWaitNs);
+        if (!ok) return;
+        tc_fence_after();
+        if (nk == 8) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_f16_ts(tmem + kColO + i * 128, tmem + kColS + i * 128 + k * 8,
-                           smem_desc(a + k * 2048, kHalf, 1024), kIdO, !(first && k == 0));
-              if (sp + lag >= jb.total || !active(jb, i, sp + lag)) mma_commit(&sm.o_full[i]);   // the slot's last
-            }
-            __syncwarp();
+          for (int k = 0; k < 4; ++k) mma_f16_ts(tO, tS + k * 8, bv + k * 128, kIdO, acc || k > 0);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < min(nk, 4); ++k) mma_f16_ts(tO, tS + k * 8, bv + k * 128, kIdO, acc || k > 0);
+        }
+        ok = mbar_wait_bounded(&sm.p_ready[i][1], np, kWaitNs);
+        np ^= 1;
+        if (!ok) return;
+        tc_fence_after();
+        if (nk == 8) {
+#pragma unroll
+          for (int k = 4; k < 8; ++k) mma_f16_ts(tO, tS + k * 8, bv + k * 128, kIdO, true);
+        } else {
+#pragma unroll 1
+          for (int k = 4; k < nk; ++k) mma_f16_ts(tO, tS + k * 8, bv + k * 128, kIdO, true);
+        }
+      };
+      // S_i = Q K^T
+      auto qk = [&](int i, uint64_t aq) {
+        const uint64_t bk = dk + ks * kStep;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
+          mma_f16_ss(tmem + kColS + i * 128, aq + off, bk + off, kIdS, k > 0);
+        }
+        mma_commit(&sm.s_full[i]);
+      };
+      auto nextV = [&] {
+        mma_commit(&sm.kv_empty[vs]);
+        vs += 2;
+        if (vs >= kStages) vs -= kStages, vp ^= 1;
+      };
+      auto nextK = [&] {
+        mma_commit(&sm.kv_empty[ks]);
+        ks += 2;
+        if (ks >= kStages) ks -= kStages, kp ^= 1;
+      };
+      while (next_job()) {
+        const Job& jb = sm.jobs[turn % kAhead];
+        const int total = jb.total, steps0 = jb.steps0, steps1 = jb.steps1;
+        const bool dual = jb.dual != 0;
+        // valid rows of the last V tile and of the one before it
+        const int ends = jb.first + total - jb.sink;                // behind the last tile
+        const int valid1 = TREE ? (ends > jb.node_tile ? jb.len : jb.cached - (ends - 1) * kTile) : jb.len - (ends - 1) * kTile;
+        const int valid2 = TREE ? jb.cached - (ends - 2) * kTile : kTile;
+        const int nk1 = min(8, (valid1 + 15) >> 4), nk2 = min(8, (valid2 + 15) >> 4);
+        const uint64_t aq1 = dq + (dual ? 0 : kStep);
+        ok = mbar_wait_bounded(&sm.q_full, jobs, kWaitNs);
+        jobs ^= 1;
+        const int lag = dual ? 2 : 1, end = total + lag;
+        // steps at which both slots have a product of each kind and whole tiles
+        const int even0 = 1, even1 = dual ? 0 : min(min(steps0, steps1), total - 1);
+        for (int s = 0; s < end && ok; ++s) {
+          if (s >= even0 && s < even1) {
+            ok = mbar_wait_bounded(&sm.kv_full[vs], vp, kWaitNs);
+            if (ok) pv(0, np0, s > 1, 8);
+            if (ok) ok = mbar_wait_bounded(&sm.kv_full[ks], kp, kWaitNs);
+            if (!ok) break;
+            qk(0, dq);
+            pv(1, np1, s > 1, 8);
+            if (!ok) break;
+            qk(1, aq1);
+            nextV();
+            nextK();
+            continue;
           }
-          if (s < jb.total && active(jb, i, s)) {
-            // S_i = Q_i K^T
-            const uint32_t n = 2 * (gs + s), st = n % kStages;
-            if (!haveK) {
-              ok = mbar_wait_bounded(&sm.kv_full[st], (n / kStages) & 1, kWaitNs);
-              haveK = true;
+          const int sp = s - lag;
+          const bool hasV = sp >= 0, hasK = s < total;
+          const int nk = sp == total - 1 ? nk1 : sp == total - 2 ? nk2 : 8;
+          if (hasV) ok = mbar_wait_bounded(&sm.kv_full[vs], vp, kWaitNs);
+          if (ok && hasK) ok = mbar_wait_bounded(&sm.kv_full[ks], kp, kWaitNs);
+#pragma unroll 1
+          for (int i = 0; i < 2 && ok; ++i) {
+            const int steps = i ? steps1 : steps0;
+            const bool turn_i = (s & 1) == i;
+            if (hasV && (dual ? turn_i : sp < steps)) {
+              uint32_t np = i ? np1 : np0;
+              pv(i, np, dual ? sp >= 2 : sp > 0, nk);
+              if (i) np1 = np;
+              else np0 = np;
+              if (!ok) break;
+              if (dual ? s >= total : s >= steps) mma_commit(&sm.o_full[i]);   // the slot's last
             }
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-              const uint32_t a = smem_u32(sq + (jb.dual ? 0 : i) * kStageBytes), bk = smem_u32(skv + st * kStageBytes);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-                mma_f16_ss(tmem + kColS + i * 128, smem_desc(a + off, 16, 1024), smem_desc(bk + off, 16, 1024), kIdS,
-                           k > 0);
-              }
-              mma_commit(&sm.s_full[i]);
-            }
-            __syncwarp();
+            if (hasK && (dual ? turn_i : s < steps)) qk(i, i ? aq1 : dq);
+          }
+          if (!ok) break;
+          if (hasV) nextV();
+          if (hasK) {
+            if (s == total - 1) mma_commit(&sm.q_empty);
+            nextK();
           }
         }
         if (!ok) break;
-        if (lane == 0) {
-          if (sp >= 0 && sp < jb.total) mma_commit(&sm.kv_empty[(2 * (gs + sp) + 1) % kStages]);
-          if (s < jb.total) mma_commit(&sm.kv_empty[(2 * (gs + s)) % kStages]);
-          if (s == jb.total - 1) mma_commit(&sm.q_empty);
-        }
-        __syncwarp();
+        mbar_arrive(&sm.job_empty[turn % kAhead]);
+        ++turn;
       }
-      gs += jb.total;
     }
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok) {
       // gave up: let the products in flight (microseconds) finish before TMEM is freed
       const uint64_t t0 = global_timer_ns();
@@ -468,65 +628,71 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     }
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRow));
     // ---------------------------------------------------------------- weights
     const int i = warp >> 2, r = tid & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + kColS + i * 128;
     const uint32_t tO = tmem + lane_base + kColO + i * 128;
     const int tok = r / p.g, hh = r - tok * p.g;
-    uint32_t ns = 0, no = 0, duals = 0;  // scores, results and joins of this slot so far
-    while (ok && walk.next(p, sm, lane, jb)) {
-      const int mine = jb.dual ? 0 : i;  // slot whose rows these are
+    uint32_t ns = 0, no = 0, duals = 0;          // scores, results and joins of this slot so far
+    uint32_t gs = 0;                             // KV tiles of the jobs before
+    while (next_job()) {
+      const Job& jb = sm.jobs[turn % kAhead];
+      const int mine = jb.dual ? 0 : i;          // slot whose rows these are
       const int place = jb.tok0 + mine * p.nt + tok;
-      const bool row_ok = tok < jb.n[mine];
+      const bool row_ok = tok < (mine ? jb.n1 : jb.n0);
       uint64_t anc = 0;
       if (TREE && row_ok && jb.first + jb.total > jb.node_tile) anc = ancestors(p.parent + jb.row0, place, p.err);
       const int cnt = slot_steps(jb, i);
       float m = -INFINITY, l = 0.f;
-      for (int x = 0; x < cnt && ok; ++x) {
-        const int s = jb.dual ? 2 * x + i : x;
-        const int t = kv_tile(jb, s);
-        ok = mbar_wait_bounded(&sm.s_full[i], ns & 1, kWaitNs);
-        ++ns;
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t v[128];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(v + 32 * q, tS + 32 * q);
-        tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) pin32(v + 32 * q);
-        // ---- mask
+      for (int x = 0; x < cnt; ++x) {
+        // ---- which of the tile's columns the row sees
+        const int c0 = kv_tile(jb, jb.dual ? 2 * x + i : x) * kTile;
         uint32_t mw[4];
         if (TREE) {
-          if (t == jb.node_tile) {
+          if (c0 >= jb.node_tile * kTile) {
             mw[0] = (uint32_t)anc;
             mw[1] = (uint32_t)(anc >> 32);
             mw[2] = mw[3] = 0;
           } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) mw[q] = low_bits(jb.cached - t * kTile - 32 * q);
+            for (int q = 0; q < 4; ++q) mw[q] = low_bits(jb.cached - c0 - 32 * q);
           }
         } else {
-          const int hi = place - t * kTile + 1;          // columns seen from the start of the tile
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            mw[q] = low_bits(hi - 32 * q);
-            if (p.local)
-              mw[q] &= ~low_bits(place - p.window + 1 - t * kTile - 32 * q) | low_bits(p.sinks - t * kTile - 32 * q);
+            mw[q] = low_bits(place + 1 - c0 - 32 * q);
+            if (p.local) mw[q] &= ~low_bits(place - p.window + 1 - c0 - 32 * q) | low_bits(p.sinks - c0 - 32 * q);
           }
         }
-        if (__any_sync(0xffffffffu, (mw[0] & mw[1] & mw[2] & mw[3]) != 0xffffffffu)) {
+        const bool masked = __any_sync(0xffffffffu, (mw[0] & mw[1] & mw[2] & mw[3]) != 0xffffffffu);
+        ok = mbar_wait_bounded(&sm.s_full[i], ns & 1, kWaitNs);
+        ++ns;
+        if (!ok) break;
+        tc_fence_after();
+        // ---- the tile's maximum.  Scores are read from TMEM twice, here and for the weights, in short
+        // loops: with all 128 in registers and the loops unrolled the row threads' code leaves no room
+        // in the instruction caches for the products' warp, whose issue then bounds the kernel (8192
+        // tokens, 32/8 heads: 586 us).
+        uint32_t v[2][32], w[16];
+        float top = -INFINITY;
+        tmem_ld32(v[0], tS);
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (!((mw[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;
+        for (int q = 0; q < 4; ++q) {
+          tmem_wait_ld();
+          pin32(v[q & 1]);
+          if (q < 3) tmem_ld32(v[(q + 1) & 1], tS + 32 * (q + 1));
+          if (masked) mask32(v[q & 1], mw[q]);
+          float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            t0 = max3(t0, __uint_as_float(v[q & 1][2 * e]), __uint_as_float(v[q & 1][2 * e + 1]));
+            t1 = max3(t1, __uint_as_float(v[q & 1][2 * e + 2]), __uint_as_float(v[q & 1][2 * e + 3]));
+          }
+          top = max3(top, t0, t1);
         }
-        // ---- reference
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int e = 0; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        tmem_ld32(v[0], tS);
         const bool grow = top * p.c > m * p.c + kGrow;   // also the first finite value (m = -inf)
         if (__any_sync(0xffffffffu, grow)) {
           const float nm = fmaxf(m, top);
@@ -536,42 +702,60 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           if (x > 0) {
             // these scores were issued after the slot's previous product, so that one is in O
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              uint32_t o[32];
-              tmem_ld32(o, tO + 32 * q);
+            for (int q = 0; q < 8; ++q) {
+              tmem_ld16(w, tO + 16 * q);
               tmem_wait_ld();
-              pin32(o);
+              pin16(w);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-              tmem_st32(tO + 32 * q, o);
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * al);
+              tmem_st16(tO + 16 * q, w);
             }
           }
         }
-        // ---- weights
+        // Rows behind the sequence in its last V tiles hold another one's values or old ones: their
+        // weights are 0, and 0 * NaN must not reach the sums.  Steps of 16 such rows are left out of the
+        // product; the rows of the last step are cleared here (by both slots: the same zeros).
+        {
+          const int valid = TREE ? (c0 >= jb.node_tile * kTile ? jb.len : jb.cached - c0) : jb.len - c0;
+          if (valid < kTile && (valid & 15)) {
+            const uint32_t n = 2 * (gs + (jb.dual ? 2 * x + i : x)) + 1, st = n % kStages;
+            ok = mbar_wait_bounded(&sm.kv_full[st], (n / kStages) & 1, kWaitNs);
+            if (!ok) break;
+            const int rows = 16 - (valid & 15);
+            for (int z = r; z < rows * 16; z += kTile) {
+              const int row = valid + (z >> 4), ch = z & 15;
+              *reinterpret_cast<uint4*>(skv + st * kStageBytes + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        // ---- weights, handed on by halves
         const float mc = m == -INFINITY ? 0.f : m * p.c;
         const uint64_t c2 = f32x2(p.c, p.c), mc2 = f32x2(-mc, -mc);
-        uint64_t sum2 = f32x2(0.f, 0.f);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t y = fma_f32x2(f32x2(__uint_as_float(v[32 * q + 2 * e]), __uint_as_float(v[32 * q + 2 * e + 1])), c2, mc2);
-            float a, b;
-            f32x2_split(y, a, b);
-            a = exp2_approx(a);
-            b = exp2_approx(b);
-            sum2 = add_f32x2(sum2, f32x2(a, b));
-            w[e] = cvt_bf16x2(a, b);
-          }
-          tmem_st16(tS + 16 * q, w);
+        uint64_t s0 = f32x2(l, 0.f), s1 = f32x2(0.f, 0.f);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          tmem_wait_ld();
+          pin32(v[0]);
+          tmem_ld32(v[1], tS + 64 * h + 32);
+          if (masked) mask32(v[0], h ? mw[2] : mw[0]);
+          weights(w, v[0], c2, mc2, s0, s1);
+          tmem_wait_ld();
+          pin32(v[1]);
+          if (h == 0) tmem_ld32(v[0], tS + 64);
+          tmem_st16(tS + 32 * h, w);
+          if (masked) mask32(v[1], h ? mw[3] : mw[1]);
+          weights(w, v[1], c2, mc2, s0, s1);
+          tmem_st16(tS + 32 * h + 16, w);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_ready[i][h]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&sm.p_full[i]);
         float a, b;
-        f32x2_split(sum2, a, b);
-        l += a + b;
+        f32x2_split(add_f32x2(s0, s1), a, b);
+        l = a + b;
       }
       if (!ok) break;
       // ---- the slot's result
@@ -581,15 +765,19 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         if (!ok) break;
         tc_fence_after();
       }
-      float a0 = 1.f, a1 = 0.f;          // factors of O0 and O1
+      float a0 = 1.f, a1 = 0.f;                  // factors of O0 and O1
       if (jb.dual) {
         if (i == 1) {
           sm.other[r] = make_float2(m, l);
           tc_fence_before();
-          mbar_arrive(&sm.m_ready);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.m_ready);
           ok = mbar_wait_bounded(&sm.m_done, duals & 1, kWaitNs);
           ++duals;
+          if (!ok) break;
           tc_fence_after();
+          gs += jb.total;
+          done_job();
           continue;
         }
         ok = mbar_wait_bounded(&sm.m_ready, duals & 1, kWaitNs);
@@ -609,59 +797,55 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           a0 *= inv;
           a1 *= inv;
         }
-        uint4* dst = nullptr;
-        if (row_ok) {
-          if (jb.direct)
-            dst = reinterpret_cast<uint4*>(p.out + ((size_t)(jb.row0 + place) * p.Hq + jb.h * p.g + hh) * 128);
-          else
-            dst = reinterpret_cast<uint4*>(p.part_o + ((size_t)jb.part * 256 + mine * 128 + r) * 128);
-        }
+        // 32 columns at a time: 64-byte lines of bf16, or 128-byte lines of fp32 partials, 4 to a row
+        const int64_t at = !row_ok ? -1
+                           : jb.direct ? ((int64_t)(jb.row0 + place) * p.Hq + jb.h * p.g + hh) * 4
+                                       : ((int64_t)jb.part * 256 + mine * 128 + r) * 4;
         if (row_ok && !jb.direct)
           reinterpret_cast<float2*>(p.part_ml)[(size_t)jb.part * 256 + mine * 128 + r] = make_float2(m, l);
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           uint32_t o[32];
           tmem_ld32(o, tO + 32 * q);
-          tmem_wait_ld();
-          pin32(o);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a0);
           if (jb.dual) {
             uint32_t o1[32];
             tmem_ld32(o1, tO + 128 + 32 * q);
             tmem_wait_ld();
+            pin32(o);
             pin32(o1);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(o1[e]) * a1);
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * a0 + __uint_as_float(o1[e]) * a1);
+          } else {
+            tmem_wait_ld();
+            pin32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a0);
           }
-          if (dst) {
-            if (jb.direct) {
+          const int64_t to = at < 0 ? at : at + q;
+          if (!TREE || jb.direct) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint4 w;
-                w.x = cvt_bf16x2(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1]));
-                w.y = cvt_bf16x2(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3]));
-                w.z = cvt_bf16x2(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5]));
-                w.w = cvt_bf16x2(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7]));
-                dst[4 * q + e] = w;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) dst[8 * q + e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
+            for (int e = 0; e < 16; ++e) o[e] = cvt_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            store_lines<4>(o, reinterpret_cast<uint4*>(p.out), to, lane);
+          } else {
+            store_lines<8>(o, reinterpret_cast<uint4*>(p.part_o), to, lane);
           }
         }
         tc_fence_before();
       }
-      if (jb.dual) mbar_arrive(&sm.m_done);
+      if (jb.dual) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.m_done);
+      }
+      gs += jb.total;
+      done_job();
     }
   }
   if (!ok && lane == 0) atomicOr(p.err, ODA_DEVERR_WAIT_TIMEOUT);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kWarpMma) {
     tc_fence_after();
     tmem_free(tmem, 512);
   }
@@ -768,15 +952,14 @@ bool aligned16(const void* a) { return (reinterpret_cast<uintptr_t>(a) & 15) == 
 size_t tile_part_rows(int n_sms) { return (size_t)2 * n_sms * 256; }
 
 oda_status prepare_tile_attention() {
-  // the kernel moves registers between its warpgroups, 208 + 208 + 88 of them a thread: the launch
-  // has to bring exactly as many
+  // the kernel moves registers between its warpgroups: the launch has to bring as many
   const void* f[2] = {reinterpret_cast<const void*>(tile_attention_kernel<false>),
                       reinterpret_cast<const void*>(tile_attention_kernel<true>)};
   for (const void* k : f) {
     cudaFuncAttributes fa;
     const oda_status a = check_cuda(cudaFuncGetAttributes(&fa, k), "cudaFuncGetAttributes(tile attention)");
     if (a != ODA_OK) return a;
-    if (fa.numRegs * 3 < 208 + 208 + 88)
+    if (fa.numRegs < kRegs)
       return set_error(ODA_ERR_UNSUPPORTED, "tile attention: built with %d registers a thread", fa.numRegs);
   }
   oda_status st = check_cuda(cudaFuncSetAttribute(tile_attention_kernel<false>,
