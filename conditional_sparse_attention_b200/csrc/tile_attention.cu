@@ -13,14 +13,17 @@
 // results are joined through tensor memory at the end: the two slots always alternate on the tensor
 // cores, one computing weights while the other's products run.
 //
-//   warps 0-3, 4-7: one thread per row of slot 0 / 1: scores from TMEM, weights back to TMEM as bf16
-//   warp 8:         issues the products S = Q K^T and O += P V (M = N = 128, 16-deep steps)
-//   warp 9:         brings Q, K and V by TMA (5 stages of 32 KB for K and V tiles)
-//   warp 10:        plans the CTA's units of work, two ahead
-//   warp 11:        idle (it completes the warpgroup whose registers go to the other two)
+//   warps 0-7, 8-15: two threads per row of slot 0 / 1, one for each 64 columns of a tile: scores from
+//                    TMEM, weights back to TMEM as bf16
+//   warp 16:         issues the products S = Q K^T and O += P V (M = N = 128, 16-deep steps)
+//   warp 17:         brings Q, K and V by TMA (5 stages of 32 KB for K and V tiles)
+//   warp 18:         plans the CTA's units of work, two ahead
+//   warp 19:         idle (it completes the warpgroup whose registers go to the others)
 //
-// TMEM: S0 | S1 | O0 | O1, 128 columns each; P_i overwrites the first 64 columns of S_i.
-// Every wait is bounded; a wait that gives up sets ODA_DEVERR_WAIT_TIMEOUT and ends the CTA.
+// TMEM: S0 | S1 | O0 | O1, 128 columns each; the weights of columns 0..63 and 64..127 overwrite columns
+// 0..31 and 64..95 of S_i, so that each thread's weights lie over its own scores.
+// Every wait is bounded; a wait that gives up sets ODA_DEVERR_WAIT_TIMEOUT and ends the CTA (the row
+// threads, which meet in pairs, go on without waiting to the end of their unit).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -36,10 +39,10 @@ constexpr int kTile = 128;              // query rows of a slot; positions of a 
 constexpr int kStages = 5;
 constexpr int kStageBytes = kTile * 256;
 constexpr int kHalf = kTile * 128;      // bytes of one 64-value half of a tile
-constexpr int kThreads = 384;           // 168 registers a thread at launch, then 200, 200 and 104 by warpgroup
-constexpr int kRegs = 168, kRegsRow = 200, kRegsOther = 104;
-static_assert(2 * kRegsRow + kRegsOther == 3 * kRegs, "the split has to add up to the launch");
-constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpPlan = 10;
+constexpr int kThreads = 640;           // 96 registers a thread at launch, then 4 x 104 and 64 by warpgroup
+constexpr int kRegs = 96, kRegsRow = 104, kRegsOther = 64;
+static_assert(4 * kRegsRow + kRegsOther == 5 * kRegs, "the split has to add up to the launch");
+constexpr int kWarpMma = 16, kWarpLoad = 17, kWarpPlan = 18;
 constexpr int kAhead = 2;               // units planned ahead
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 8.0f;           // log2 of the growth that moves a row's reference
@@ -88,7 +91,8 @@ struct Smem {
   uint64_t s_full[2], p_ready[2][2], o_full[2];
   uint64_t m_ready, m_done;
   uint64_t job_full[kAhead], job_empty[kAhead];
-  float2 other[kTile];                  // slot 1's reference and sum where the slots are joined
+  float pair[2][kTile];                 // what the two threads of a row tell each other
+  float join_m[kTile];                  // slot 1's references where the slots are joined (sums: in pair)
   Job jobs[kAhead];
   uint32_t tmem;
   uint32_t pref[ODA_MAX_BATCH + 1];     // prompt: blocks of each sequence; tree: tiles before it
@@ -280,10 +284,10 @@ __device__ __forceinline__ void exp2_pair(uint64_t x2, float& a, float& b) {
   b = __uint_as_float(__float_as_uint(b) + (__float_as_uint(tb) << 23));
 }
 
-// Weights 2^(c v - mc) of 32 columns as bf16 pairs, and their sums (unrounded) added to s0, s1.  The
-// exponential unit makes 16 a clock and SM, 2048 clocks for the two slots' tiles, as long as the tile's
-// products: one pair in kPoly goes to the FMA pipe.
-__device__ __forceinline__ void weights(uint32_t* w, const uint32_t* v, uint64_t c2, uint64_t mc2, uint64_t& s0, uint64_t& s1) {
+// Weights 2^(c v - mc) of 32 columns as bf16 pairs, which take the scores' registers, and their sums
+// (unrounded) added to s0, s1.  The exponential unit makes 16 a clock and SM, 2048 clocks for the two
+// slots' tiles, as long as the tile's products: one pair in kPoly goes to the FMA pipe.
+__device__ __forceinline__ void weights(uint32_t* v, uint64_t c2, uint64_t mc2, uint64_t& s0, uint64_t& s1) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const uint64_t x2 = fma_f32x2(f32x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), c2, mc2);
@@ -297,8 +301,17 @@ __device__ __forceinline__ void weights(uint32_t* w, const uint32_t* v, uint64_t
     }
     if (e & 1) s1 = add_f32x2(s1, f32x2(a, b));
     else s0 = add_f32x2(s0, f32x2(a, b));
-    w[e] = cvt_bf16x2(a, b);
+    v[e] = cvt_bf16x2(a, b);
   }
+}
+
+// The two warps that share 32 rows meet: plainly, or with the OR of a predicate.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_or(int id, bool x) {
+  uint32_t y;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.or.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(y) : "r"(id), "r"((uint32_t)x) : "memory");
+  return y != 0;
 }
 
 // Masked ones of 32 scores to -inf.
@@ -360,11 +373,11 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       mbar_init(&sm.p_ready[i][1], 4);
       mbar_init(&sm.o_full[i], 1);
     }
-    mbar_init(&sm.m_ready, 4);
-    mbar_init(&sm.m_done, 4);
+    mbar_init(&sm.m_ready, 8);
+    mbar_init(&sm.m_done, 8);
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(&sm.job_full[i], 1);
-      mbar_init(&sm.job_empty[i], 10);
+      mbar_init(&sm.job_empty[i], 18);
     }
     fence_mbar_init();
   }
@@ -439,21 +452,30 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   } else if (warp == kWarpLoad) {
     // ------------------------------------------------------------------ loads
     uint32_t gs = 0, jobs = 0;           // KV tiles (K, V counted apart: 2 gs) and jobs so far
+    const int pg = (lane >> 1) & 7, hf = lane & 1;      // tree: lanes 0-15 bring 8 pages x 2 halves
     while (next_job()) {
       const Job& jb = sm.jobs[turn % kAhead];
+      // the page-table entries are read a tile ahead of the copies that wait for them
+      auto entry = [&](int t) {
+        const int at = t * 8 + pg;
+        return t < jb.node_tile && at * 16 < jb.cached ? p.page_table[(size_t)jb.b * p.max_pages + at] : -1;
+      };
+      int phys = TREE ? entry(jb.first) : 0;
       if (jobs > 0) ok = mbar_wait_bounded(&sm.q_empty, (jobs - 1) & 1, kWaitNs);
       if (!ok) break;
       if (lane == 0) {
         const int slots = jb.n1 > 0 ? 2 : 1;
         mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(slots * 2 * 128 * p.g * p.nt));
         for (int i = 0; i < slots; ++i)
-          for (int hf = 0; hf < 2; ++hf)
-            tma_load_3d(sq + i * kStageBytes + hf * kHalf, &mq, hf * 64, jb.h * p.g, jb.row0 + jb.tok0 + i * p.nt,
+          for (int h2 = 0; h2 < 2; ++h2)
+            tma_load_3d(sq + i * kStageBytes + h2 * kHalf, &mq, h2 * 64, jb.h * p.g, jb.row0 + jb.tok0 + i * p.nt,
                         &sm.q_full);
       }
       ++jobs;
       for (int s = 0; s < jb.total && ok; ++s, ++gs) {
         const int t = kv_tile(jb, s);
+        const int page = phys;
+        if (TREE) phys = entry(t + 1);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const uint32_t n = 2 * gs + w, st = n % kStages;
@@ -463,25 +485,22 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           if (!TREE) {
             if (lane == 0) {
               mbar_arrive_expect_tx(&sm.kv_full[st], kStageBytes);
-              for (int hf = 0; hf < 2; ++hf)
-                tma_load_3d(dst + hf * kHalf, w ? &mv : &mk, hf * 64, jb.h, jb.row0 + t * kTile, &sm.kv_full[st]);
+              for (int h2 = 0; h2 < 2; ++h2)
+                tma_load_3d(dst + h2 * kHalf, w ? &mv : &mk, h2 * 64, jb.h, jb.row0 + t * kTile, &sm.kv_full[st]);
             }
           } else if (t == jb.node_tile) {
             if (lane == 0) {
               mbar_arrive_expect_tx(&sm.kv_full[st], ODA_MAX_TREE * 256);
-              for (int hf = 0; hf < 2; ++hf)
-                tma_load_3d(dst + hf * kHalf, w ? &mvn : &mkn, hf * 64, jb.h, jb.row0, &sm.kv_full[st]);
+              for (int h2 = 0; h2 < 2; ++h2)
+                tma_load_3d(dst + h2 * kHalf, w ? &mvn : &mkn, h2 * 64, jb.h, jb.row0, &sm.kv_full[st]);
             }
           } else {
-            // 8 pages x 2 halves of 16 rows x 64 values; lane = page * 2 + half
             const int pages = min(8, (jb.cached - t * kTile + 15) / 16);
-            const int pg = lane >> 1, hf = lane & 1;
             if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[st], (uint32_t)(pages * 4096));
             __syncwarp();
-            if (pg < pages) {
-              const int64_t phys = p.page_table[(size_t)jb.b * p.max_pages + t * 8 + pg];
-              int64_t row = (phys * p.Hkv + jb.h) * 16;
-              if (phys < 0 || phys >= p.n_pages) {
+            if (lane < 2 * pages) {
+              int64_t row = ((int64_t)page * p.Hkv + jb.h) * 16;
+              if (page < 0 || page >= p.n_pages) {
                 atomicOr(p.err, ODA_DEVERR_PAGE_RANGE);
                 row = p.n_pages * p.Hkv * 16;           // past the pool: the copy fills zeros
               }
@@ -533,10 +552,10 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         tc_fence_after();
         if (nk == 8) {
 #pragma unroll
-          for (int k = 4; k < 8; ++k) mma_f16_ts(tO, tS + k * 8, bv + k * 128, kIdO, true);
+          for (int k = 4; k < 8; ++k) mma_f16_ts(tO, tS + 32 + k * 8, bv + k * 128, kIdO, true);
         } else {
 #pragma unroll 1
-          for (int k = 4; k < nk; ++k) mma_f16_ts(tO, tS + k * 8, bv + k * 128, kIdO, true);
+          for (int k = 4; k < nk; ++k) mma_f16_ts(tO, tS + 32 + k * 8, bv + k * 128, kIdO, true);
         }
       };
       // S_i = Q K^T
@@ -630,14 +649,17 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRow));
     // ---------------------------------------------------------------- weights
-    const int i = warp >> 2, r = tid & 127;
+    const int i = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
+    const int meet = 1 + i * 4 + (warp & 3);     // barrier of the two warps of these rows
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_base + kColS + i * 128;
-    const uint32_t tO = tmem + lane_base + kColO + i * 128;
-    const int tok = r / p.g, hh = r - tok * p.g;
+    const uint32_t tS = tmem + lane_base + kColS + i * 128 + half * 64;
+    const uint32_t tO = tmem + lane_base + kColO + i * 128 + half * 64;
+    const int tok = r / p.g;
     uint32_t ns = 0, no = 0, duals = 0;          // scores, results and joins of this slot so far
     uint32_t gs = 0;                             // KV tiles of the jobs before
-    while (next_job()) {
+    while (true) {
+      const bool more = next_job();
+      if (pair_or(meet, !ok) || !more) break;    // both warps of a pair go on, or neither
       const Job& jb = sm.jobs[turn % kAhead];
       const int mine = jb.dual ? 0 : i;          // slot whose rows these are
       const int place = jb.tok0 + mine * p.nt + tok;
@@ -647,62 +669,62 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       const int cnt = slot_steps(jb, i);
       float m = -INFINITY, l = 0.f;
       for (int x = 0; x < cnt; ++x) {
-        // ---- which of the tile's columns the row sees
-        const int c0 = kv_tile(jb, jb.dual ? 2 * x + i : x) * kTile;
-        uint32_t mw[4];
+        // ---- which of this thread's columns the row sees
+        const int t0 = kv_tile(jb, jb.dual ? 2 * x + i : x) * kTile, c0 = t0 + half * 64;
+        uint32_t mw0, mw1;
         if (TREE) {
-          if (c0 >= jb.node_tile * kTile) {
-            mw[0] = (uint32_t)anc;
-            mw[1] = (uint32_t)(anc >> 32);
-            mw[2] = mw[3] = 0;
+          if (t0 >= jb.node_tile * kTile) {
+            mw0 = half ? 0u : (uint32_t)anc;
+            mw1 = half ? 0u : (uint32_t)(anc >> 32);
           } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) mw[q] = low_bits(jb.cached - c0 - 32 * q);
+            mw0 = low_bits(jb.cached - c0);
+            mw1 = low_bits(jb.cached - c0 - 32);
           }
         } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            mw[q] = low_bits(place + 1 - c0 - 32 * q);
-            if (p.local) mw[q] &= ~low_bits(place - p.window + 1 - c0 - 32 * q) | low_bits(p.sinks - c0 - 32 * q);
+          mw0 = low_bits(place + 1 - c0);
+          mw1 = low_bits(place + 1 - c0 - 32);
+          if (p.local) {
+            mw0 &= ~low_bits(place - p.window + 1 - c0) | low_bits(p.sinks - c0);
+            mw1 &= ~low_bits(place - p.window + 1 - c0 - 32) | low_bits(p.sinks - c0 - 32);
           }
         }
-        const bool masked = __any_sync(0xffffffffu, (mw[0] & mw[1] & mw[2] & mw[3]) != 0xffffffffu);
-        ok = mbar_wait_bounded(&sm.s_full[i], ns & 1, kWaitNs);
+        const bool masked = __any_sync(0xffffffffu, (mw0 & mw1) != 0xffffffffu);
+        if (ok) ok = mbar_wait_bounded(&sm.s_full[i], ns & 1, kWaitNs);
         ++ns;
-        if (!ok) break;
         tc_fence_after();
-        // ---- the tile's maximum.  Scores are read from TMEM twice, here and for the weights, in short
-        // loops: with all 128 in registers and the loops unrolled the row threads' code leaves no room
-        // in the instruction caches for the products' warp, whose issue then bounds the kernel (8192
-        // tokens, 32/8 heads: 586 us).
-        uint32_t v[2][32], w[16];
-        float top = -INFINITY;
-        tmem_ld32(v[0], tS);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          tmem_wait_ld();
-          pin32(v[q & 1]);
-          if (q < 3) tmem_ld32(v[(q + 1) & 1], tS + 32 * (q + 1));
-          if (masked) mask32(v[q & 1], mw[q]);
-          float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            t0 = max3(t0, __uint_as_float(v[q & 1][2 * e]), __uint_as_float(v[q & 1][2 * e + 1]));
-            t1 = max3(t1, __uint_as_float(v[q & 1][2 * e + 2]), __uint_as_float(v[q & 1][2 * e + 3]));
-          }
-          top = max3(top, t0, t1);
+        // ---- the maximum
+        uint32_t v[64];
+        tmem_ld32(v, tS);
+        tmem_ld32(v + 32, tS + 32);
+        tmem_wait_ld();
+        pin32(v);
+        pin32(v + 32);
+        if (masked) {
+          mask32(v, mw0);
+          mask32(v + 32, mw1);
         }
-        tmem_ld32(v[0], tS);
+        float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          top0 = max3(top0, __uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]));
+          top1 = max3(top1, __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+        }
+        const float top = fmaxf(top0, top1);
         const bool grow = top * p.c > m * p.c + kGrow;   // also the first finite value (m = -inf)
-        if (__any_sync(0xffffffffu, grow)) {
-          const float nm = fmaxf(m, top);
+        if (pair_or(meet, grow)) {
+          if (half) sm.pair[i][r] = top;
+          pair_sync(meet);
+          if (!half) sm.pair[i][r] = max3(m, top, sm.pair[i][r]);
+          pair_sync(meet);
+          const float nm = sm.pair[i][r];
           const float al = m == nm ? 1.f : exp2_approx((m - nm) * p.c);
           m = nm;
           l *= al;
           if (x > 0) {
             // these scores were issued after the slot's previous product, so that one is in O
 #pragma unroll 1
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[16];
               tmem_ld16(w, tO + 16 * q);
               tmem_wait_ld();
               pin16(w);
@@ -716,13 +738,12 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         // weights are 0, and 0 * NaN must not reach the sums.  Steps of 16 such rows are left out of the
         // product; the rows of the last step are cleared here (by both slots: the same zeros).
         {
-          const int valid = TREE ? (c0 >= jb.node_tile * kTile ? jb.len : jb.cached - c0) : jb.len - c0;
+          const int valid = TREE ? (t0 >= jb.node_tile * kTile ? jb.len : jb.cached - t0) : jb.len - t0;
           if (valid < kTile && (valid & 15)) {
             const uint32_t n = 2 * (gs + (jb.dual ? 2 * x + i : x)) + 1, st = n % kStages;
-            ok = mbar_wait_bounded(&sm.kv_full[st], (n / kStages) & 1, kWaitNs);
-            if (!ok) break;
+            if (ok) ok = mbar_wait_bounded(&sm.kv_full[st], (n / kStages) & 1, kWaitNs);
             const int rows = 16 - (valid & 15);
-            for (int z = r; z < rows * 16; z += kTile) {
+            for (int z = half * kTile + r; z < rows * 16; z += 2 * kTile) {
               const int row = valid + (z >> 4), ch = z & 15;
               *reinterpret_cast<uint4*>(skv + st * kStageBytes + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
                   make_uint4(0, 0, 0, 0);
@@ -730,66 +751,55 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             fence_proxy_async_smem();
           }
         }
-        // ---- weights, handed on by halves
+        // ---- weights
         const float mc = m == -INFINITY ? 0.f : m * p.c;
         const uint64_t c2 = f32x2(p.c, p.c), mc2 = f32x2(-mc, -mc);
         uint64_t s0 = f32x2(l, 0.f), s1 = f32x2(0.f, 0.f);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          tmem_wait_ld();
-          pin32(v[0]);
-          tmem_ld32(v[1], tS + 64 * h + 32);
-          if (masked) mask32(v[0], h ? mw[2] : mw[0]);
-          weights(w, v[0], c2, mc2, s0, s1);
-          tmem_wait_ld();
-          pin32(v[1]);
-          if (h == 0) tmem_ld32(v[0], tS + 64);
-          tmem_st16(tS + 32 * h, w);
-          if (masked) mask32(v[1], h ? mw[3] : mw[1]);
-          weights(w, v[1], c2, mc2, s0, s1);
-          tmem_st16(tS + 32 * h + 16, w);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.p_ready[i][h]);
-        }
+        weights(v, c2, mc2, s0, s1);
+        tmem_st16(tS, v);
+        weights(v + 32, c2, mc2, s0, s1);
+        tmem_st16(tS + 16, v + 32);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready[i][half]);
         float a, b;
         f32x2_split(add_f32x2(s0, s1), a, b);
         l = a + b;
       }
-      if (!ok) break;
       // ---- the slot's result
       if (cnt > 0) {
-        ok = mbar_wait_bounded(&sm.o_full[i], no & 1, kWaitNs);
+        if (ok) ok = mbar_wait_bounded(&sm.o_full[i], no & 1, kWaitNs);
         ++no;
-        if (!ok) break;
         tc_fence_after();
+        if (half) sm.pair[i][r] = l;
+        pair_sync(meet);
+        if (!half) sm.pair[i][r] += l;
+        pair_sync(meet);
+        l = sm.pair[i][r];
       }
       float a0 = 1.f, a1 = 0.f;                  // factors of O0 and O1
       if (jb.dual) {
         if (i == 1) {
-          sm.other[r] = make_float2(m, l);
+          if (!half) sm.join_m[r] = m;
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.m_ready);
-          ok = mbar_wait_bounded(&sm.m_done, duals & 1, kWaitNs);
+          if (ok) ok = mbar_wait_bounded(&sm.m_done, duals & 1, kWaitNs);
           ++duals;
-          if (!ok) break;
           tc_fence_after();
           gs += jb.total;
           done_job();
           continue;
         }
-        ok = mbar_wait_bounded(&sm.m_ready, duals & 1, kWaitNs);
+        if (ok) ok = mbar_wait_bounded(&sm.m_ready, duals & 1, kWaitNs);
         ++duals;
-        if (!ok) break;
         tc_fence_after();
-        const float2 ml = sm.other[r];
-        const float nm = fmaxf(m, ml.x);
+        const float m1 = sm.join_m[r], nm = fmaxf(m, m1);
         a0 = m == nm ? 1.f : exp2_approx((m - nm) * p.c);
-        a1 = ml.x == nm ? 1.f : exp2_approx((ml.x - nm) * p.c);
+        a1 = m1 == nm ? 1.f : exp2_approx((m1 - nm) * p.c);
         m = nm;
-        l = l * a0 + ml.y * a1;
+        l = l * a0 + sm.pair[1][r] * a1;
       }
       if (cnt > 0) {
         if (jb.direct) {
@@ -798,29 +808,28 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           a1 *= inv;
         }
         // 32 columns at a time: 64-byte lines of bf16, or 128-byte lines of fp32 partials, 4 to a row
+        const int hh = r - tok * p.g;
         const int64_t at = !row_ok ? -1
-                           : jb.direct ? ((int64_t)(jb.row0 + place) * p.Hq + jb.h * p.g + hh) * 4
-                                       : ((int64_t)jb.part * 256 + mine * 128 + r) * 4;
-        if (row_ok && !jb.direct)
+                           : (jb.direct ? ((int64_t)(jb.row0 + place) * p.Hq + jb.h * p.g + hh) * 4
+                                        : ((int64_t)jb.part * 256 + mine * 128 + r) * 4) + half * 2;
+        if (row_ok && !jb.direct && !half)
           reinterpret_cast<float2*>(p.part_ml)[(size_t)jb.part * 256 + mine * 128 + r] = make_float2(m, l);
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           uint32_t o[32];
           tmem_ld32(o, tO + 32 * q);
+          tmem_wait_ld();
+          pin32(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a0);
           if (jb.dual) {
             uint32_t o1[32];
             tmem_ld32(o1, tO + 128 + 32 * q);
             tmem_wait_ld();
-            pin32(o);
             pin32(o1);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint(__uint_as_float(o[e]) * a0 + __uint_as_float(o1[e]) * a1);
-          } else {
-            tmem_wait_ld();
-            pin32(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a0);
+              o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(o1[e]) * a1);
           }
           const int64_t to = at < 0 ? at : at + q;
           if (!TREE || jb.direct) {
