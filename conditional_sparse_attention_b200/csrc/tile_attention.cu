@@ -16,9 +16,8 @@
 //   warps 0-7, 8-15: two threads per row of slot 0 / 1, one for each 64 columns of a tile: scores from
 //                    TMEM, weights back to TMEM as bf16
 //   warp 16:         issues the products S = Q K^T and O += P V (M = N = 128, 16-deep steps)
-//   warp 17:         brings Q, K and V by TMA (5 stages of 32 KB for K and V tiles)
+//   warps 17, 19:    bring Q and K, and V, by TMA (a ring of 5 stages of 32 KB, in the order of use)
 //   warp 18:         plans the CTA's units of work, two ahead
-//   warp 19:         idle (it completes the warpgroup whose registers go to the others)
 //
 // TMEM: S0 | S1 | O0 | O1, 128 columns each; the weights of columns 0..63 and 64..127 overwrite columns
 // 0..31 and 64..95 of S_i, so that each thread's weights lie over its own scores.
@@ -42,7 +41,7 @@ constexpr int kHalf = kTile * 128;      // bytes of one 64-value half of a tile
 constexpr int kThreads = 640;           // 96 registers a thread at launch, then 4 x 104 and 64 by warpgroup
 constexpr int kRegs = 96, kRegsRow = 104, kRegsOther = 64;
 static_assert(4 * kRegsRow + kRegsOther == 5 * kRegs, "the split has to add up to the launch");
-constexpr int kWarpMma = 16, kWarpLoad = 17, kWarpPlan = 18;
+constexpr int kWarpMma = 16, kWarpLoad = 17, kWarpPlan = 18, kWarpLoadV = 19;
 constexpr int kAhead = 2;               // units planned ahead
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 8.0f;           // log2 of the growth that moves a row's reference
@@ -102,6 +101,10 @@ constexpr int kDynBytes = kTileBytes + sizeof(Smem);
 static_assert(kDynBytes <= 227 * 1024, "shared memory of a CTA");
 
 __device__ __forceinline__ int kv_tile(const Job& j, int s) { return (j.sink && s == 0) ? 0 : j.first + s - j.sink; }
+// Place of a step's K and V tile in the job's order of use: K0 | V0 K1 | V1 K2 ..., and where the slots
+// alternate on the tiles of one, whose products with V come two steps later, K0 | K1 | V0 K2 | V1 K3 ...
+__device__ __forceinline__ uint32_t order_k(const Job& j, int s) { return j.dual && s > 0 ? 2 * s - 1 : 2 * s; }
+__device__ __forceinline__ uint32_t order_v(const Job& j, int s) { return j.dual && s < j.total - 1 ? 2 * s + 2 : 2 * s + 1; }
 __device__ __forceinline__ int slot_steps(const Job& j, int i) { return j.dual ? (j.total + 1 - i) >> 1 : i ? j.steps1 : j.steps0; }
 
 __device__ __forceinline__ int seq_len(const TileParams& p, int b, int most, bool report) {
@@ -377,7 +380,7 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     mbar_init(&sm.m_done, 8);
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(&sm.job_full[i], 1);
-      mbar_init(&sm.job_empty[i], 18);
+      mbar_init(&sm.job_empty[i], 19);
     }
     fence_mbar_init();
   }
@@ -449,8 +452,9 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       __syncwarp();
       if (!more) break;
     }
-  } else if (warp == kWarpLoad) {
+  } else if (warp == kWarpLoad || warp == kWarpLoadV) {
     // ------------------------------------------------------------------ loads
+    const int w = warp == kWarpLoadV;    // K or V tiles
     uint32_t gs = 0, jobs = 0;           // KV tiles (K, V counted apart: 2 gs) and jobs so far
     const int pg = (lane >> 1) & 7, hf = lane & 1;      // tree: lanes 0-15 bring 8 pages x 2 halves
     while (next_job()) {
@@ -461,63 +465,63 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         return t < jb.node_tile && at * 16 < jb.cached ? p.page_table[(size_t)jb.b * p.max_pages + at] : -1;
       };
       int phys = TREE ? entry(jb.first) : 0;
-      if (jobs > 0) ok = mbar_wait_bounded(&sm.q_empty, (jobs - 1) & 1, kWaitNs);
-      if (!ok) break;
-      if (lane == 0) {
-        const int slots = jb.n1 > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(slots * 2 * 128 * p.g * p.nt));
-        for (int i = 0; i < slots; ++i)
-          for (int h2 = 0; h2 < 2; ++h2)
-            tma_load_3d(sq + i * kStageBytes + h2 * kHalf, &mq, h2 * 64, jb.h * p.g, jb.row0 + jb.tok0 + i * p.nt,
-                        &sm.q_full);
+      if (w == 0) {
+        if (jobs > 0) ok = mbar_wait_bounded(&sm.q_empty, (jobs - 1) & 1, kWaitNs);
+        if (!ok) break;
+        if (lane == 0) {
+          const int slots = jb.n1 > 0 ? 2 : 1;
+          mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(slots * 2 * 128 * p.g * p.nt));
+          for (int i = 0; i < slots; ++i)
+            for (int h2 = 0; h2 < 2; ++h2)
+              tma_load_3d(sq + i * kStageBytes + h2 * kHalf, &mq, h2 * 64, jb.h * p.g, jb.row0 + jb.tok0 + i * p.nt,
+                          &sm.q_full);
+        }
       }
       ++jobs;
-      for (int s = 0; s < jb.total && ok; ++s, ++gs) {
+      for (int s = 0; s < jb.total; ++s) {
         const int t = kv_tile(jb, s);
         const int page = phys;
         if (TREE) phys = entry(t + 1);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const uint32_t n = 2 * gs + w, st = n % kStages;
-          if (n >= kStages) ok = mbar_wait_bounded(&sm.kv_empty[st], (n / kStages - 1) & 1, kWaitNs);
-          if (!ok) break;
-          uint8_t* dst = skv + st * kStageBytes;
-          if (!TREE) {
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&sm.kv_full[st], kStageBytes);
-              for (int h2 = 0; h2 < 2; ++h2)
-                tma_load_3d(dst + h2 * kHalf, w ? &mv : &mk, h2 * 64, jb.h, jb.row0 + t * kTile, &sm.kv_full[st]);
-            }
-          } else if (t == jb.node_tile) {
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&sm.kv_full[st], ODA_MAX_TREE * 256);
-              for (int h2 = 0; h2 < 2; ++h2)
-                tma_load_3d(dst + h2 * kHalf, w ? &mvn : &mkn, h2 * 64, jb.h, jb.row0, &sm.kv_full[st]);
-            }
-          } else {
-            const int pages = min(8, (jb.cached - t * kTile + 15) / 16);
-            if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[st], (uint32_t)(pages * 4096));
-            __syncwarp();
-            if (lane < 2 * pages) {
-              int64_t row = ((int64_t)page * p.Hkv + jb.h) * 16;
-              if (page < 0 || page >= p.n_pages) {
-                atomicOr(p.err, ODA_DEVERR_PAGE_RANGE);
-                row = p.n_pages * p.Hkv * 16;           // past the pool: the copy fills zeros
-              }
-              tma_load_2d(dst + hf * kHalf + pg * 2048, w ? &mv : &mk, hf * 64, (int32_t)row, &sm.kv_full[st]);
-            }
-          }
-          __syncwarp();
-        }
+        const uint32_t n = 2 * gs + (w ? order_v(jb, s) : order_k(jb, s)), st = n % kStages;
+        if (n >= kStages) ok = mbar_wait_bounded(&sm.kv_empty[st], (n / kStages - 1) & 1, kWaitNs);
         if (!ok) break;
+        uint8_t* dst = skv + st * kStageBytes;
+        if (!TREE) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.kv_full[st], kStageBytes);
+            for (int h2 = 0; h2 < 2; ++h2)
+              tma_load_3d(dst + h2 * kHalf, w ? &mv : &mk, h2 * 64, jb.h, jb.row0 + t * kTile, &sm.kv_full[st]);
+          }
+        } else if (t == jb.node_tile) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.kv_full[st], ODA_MAX_TREE * 256);
+            for (int h2 = 0; h2 < 2; ++h2)
+              tma_load_3d(dst + h2 * kHalf, w ? &mvn : &mkn, h2 * 64, jb.h, jb.row0, &sm.kv_full[st]);
+          }
+        } else {
+          const int pages = min(8, (jb.cached - t * kTile + 15) / 16);
+          if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[st], (uint32_t)(pages * 4096));
+          __syncwarp();
+          if (lane < 2 * pages) {
+            int64_t row = ((int64_t)page * p.Hkv + jb.h) * 16;
+            if (page < 0 || page >= p.n_pages) {
+              atomicOr(p.err, ODA_DEVERR_PAGE_RANGE);
+              row = p.n_pages * p.Hkv * 16;             // past the pool: the copy fills zeros
+            }
+            tma_load_2d(dst + hf * kHalf + pg * 2048, w ? &mv : &mk, hf * 64, (int32_t)row, &sm.kv_full[st]);
+          }
+        }
+        __syncwarp();
       }
+      if (!ok) break;
+      gs += jb.total;
       done_job();
     }
-    if (!ok) {   // gave up: let the copies in flight land before the CTA ends
-      const uint32_t n = 2 * gs;
-      for (uint32_t i = n >= kStages ? n - kStages : 0; i < n; ++i)
-        mbar_wait_bounded(&sm.kv_full[i % kStages], (i / kStages) & 1, kWaitNs);
-      if (jobs > 0) mbar_wait_bounded(&sm.q_full, (jobs - 1) & 1, kWaitNs);
+    if (!ok) {
+      // gave up: let the copies in flight (microseconds) land before the CTA ends
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 1000000ull) {
+      }
     }
   } else if (warp == kWarpMma) {
     // --------------------------------------------------------------- products
@@ -530,12 +534,12 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       const uint64_t dq = smem_desc(smem_u32(sq), 16, 1024), dk = smem_desc(smem_u32(skv), 16, 1024);
       const uint64_t dv = smem_desc(smem_u32(skv), kHalf, 1024);
       constexpr uint32_t kStep = kStageBytes >> 4;  // of a descriptor's address
-      uint32_t ks = 0, kp = 0, vs = 1, vp = 0;      // stage and phase of the next K and V tile
+      uint32_t st = 0, ph = 0;                      // stage and phase of the next tile in the order of use
       uint32_t np0 = 0, np1 = 0, jobs = 0;          // parity of each slot's weights consumed; of the jobs
       // O_i += P_i V: the first 64 weights of every row, then the others; nk = 16-row steps of the tile
-      auto pv = [&](int i, uint32_t& np, bool acc, int nk) {
+      auto pv = [&](int i, uint32_t& np, uint32_t at, bool acc, int nk) {
         const uint32_t tS = tmem + kColS + i * 128, tO = tmem + kColO + i * 128;
-        const uint64_t bv = dv + vs * kStep;
+        const uint64_t bv = dv + at * kStep;
         ok = mbar_wait_bounded(&sm.p_ready[i][0], np, kWaitNs);
         if (!ok) return;
         tc_fence_after();
@@ -559,8 +563,8 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         }
       };
       // S_i = Q K^T
-      auto qk = [&](int i, uint64_t aq) {
-        const uint64_t bk = dk + ks * kStep;
+      auto qk = [&](int i, uint64_t aq, uint32_t at) {
+        const uint64_t bk = dk + at * kStep;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const uint32_t off = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
@@ -568,15 +572,8 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         }
         mma_commit(&sm.s_full[i]);
       };
-      auto nextV = [&] {
-        mma_commit(&sm.kv_empty[vs]);
-        vs += 2;
-        if (vs >= kStages) vs -= kStages, vp ^= 1;
-      };
-      auto nextK = [&] {
-        mma_commit(&sm.kv_empty[ks]);
-        ks += 2;
-        if (ks >= kStages) ks -= kStages, kp ^= 1;
+      auto next = [&] {
+        if (++st == kStages) st = 0, ph ^= 1;
       };
       while (next_job()) {
         const Job& jb = sm.jobs[turn % kAhead];
@@ -595,43 +592,58 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         const int even0 = 1, even1 = dual ? 0 : min(min(steps0, steps1), total - 1);
         for (int s = 0; s < end && ok; ++s) {
           if (s >= even0 && s < even1) {
-            ok = mbar_wait_bounded(&sm.kv_full[vs], vp, kWaitNs);
-            if (ok) pv(0, np0, s > 1, 8);
-            if (ok) ok = mbar_wait_bounded(&sm.kv_full[ks], kp, kWaitNs);
+            const uint32_t vs = st;
+            ok = mbar_wait_bounded(&sm.kv_full[st], ph, kWaitNs);
+            if (ok) pv(0, np0, vs, s > 1, 8);
+            next();
+            if (ok) ok = mbar_wait_bounded(&sm.kv_full[st], ph, kWaitNs);
             if (!ok) break;
-            qk(0, dq);
-            pv(1, np1, s > 1, 8);
+            qk(0, dq, st);
+            pv(1, np1, vs, s > 1, 8);
             if (!ok) break;
-            qk(1, aq1);
-            nextV();
-            nextK();
+            qk(1, aq1, st);
+            mma_commit(&sm.kv_empty[vs]);
+            mma_commit(&sm.kv_empty[st]);
+            next();
             continue;
           }
           const int sp = s - lag;
           const bool hasV = sp >= 0, hasK = s < total;
           const int nk = sp == total - 1 ? nk1 : sp == total - 2 ? nk2 : 8;
-          if (hasV) ok = mbar_wait_bounded(&sm.kv_full[vs], vp, kWaitNs);
-          if (ok && hasK) ok = mbar_wait_bounded(&sm.kv_full[ks], kp, kWaitNs);
+          uint32_t vs = 0, ks = 0, kph = 0;
+          bool kwait = hasK;
+          if (hasV) {
+            vs = st;
+            ok = mbar_wait_bounded(&sm.kv_full[st], ph, kWaitNs);
+            next();
+          }
+          if (hasK) {
+            ks = st;
+            kph = ph;
+            next();
+          }
 #pragma unroll 1
           for (int i = 0; i < 2 && ok; ++i) {
             const int steps = i ? steps1 : steps0;
             const bool turn_i = (s & 1) == i;
             if (hasV && (dual ? turn_i : sp < steps)) {
               uint32_t np = i ? np1 : np0;
-              pv(i, np, dual ? sp >= 2 : sp > 0, nk);
+              pv(i, np, vs, dual ? sp >= 2 : sp > 0, nk);
               if (i) np1 = np;
               else np0 = np;
               if (!ok) break;
               if (dual ? s >= total : s >= steps) mma_commit(&sm.o_full[i]);   // the slot's last
             }
-            if (hasK && (dual ? turn_i : s < steps)) qk(i, i ? aq1 : dq);
+            if (hasK && (dual ? turn_i : s < steps)) {
+              if (kwait) ok = mbar_wait_bounded(&sm.kv_full[ks], kph, kWaitNs);
+              kwait = false;
+              if (ok) qk(i, i ? aq1 : dq, ks);
+            }
           }
           if (!ok) break;
-          if (hasV) nextV();
-          if (hasK) {
-            if (s == total - 1) mma_commit(&sm.q_empty);
-            nextK();
-          }
+          if (hasV) mma_commit(&sm.kv_empty[vs]);
+          if (hasK) mma_commit(&sm.kv_empty[ks]);
+          if (s == total - 1) mma_commit(&sm.q_empty);
         }
         if (!ok) break;
         mbar_arrive(&sm.job_empty[turn % kAhead]);
@@ -740,7 +752,7 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         {
           const int valid = TREE ? (t0 >= jb.node_tile * kTile ? jb.len : jb.cached - t0) : jb.len - t0;
           if (valid < kTile && (valid & 15)) {
-            const uint32_t n = 2 * (gs + (jb.dual ? 2 * x + i : x)) + 1, st = n % kStages;
+            const uint32_t n = 2 * gs + order_v(jb, jb.dual ? 2 * x + i : x), st = n % kStages;
             if (ok) ok = mbar_wait_bounded(&sm.kv_full[st], (n / kStages) & 1, kWaitNs);
             const int rows = 16 - (valid & 15);
             for (int z = half * kTile + r; z < rows * 16; z += 2 * kTile) {
