@@ -118,34 +118,39 @@ __device__ __forceinline__ int seq_len(const TileParams& p, int b, int most, boo
 
 // Prompt work: block j of a sequence is its tokens [2 nt j, 2 nt (j + 1)); units are (block, KV head),
 // ordered by falling block index over all sequences (the longest rows first), KV heads innermost.
-// pref holds every sequence's block count.  Called by a whole warp.
+// pref holds every sequence's block count.  Called by a whole warp.  (Loops are kept rolled: a CTA
+// runs this code before its first copy, at the pace of its instruction fetch.)
 __device__ __forceinline__ uint32_t blocks_from(const Smem& sm, int n_seqs, uint32_t j, int lane) {
   uint32_t s = 0;
-  for (int b = lane; b < n_seqs; b += 32) {
-    const uint32_t nb = sm.pref[b];
-    s += nb > j ? nb - j : 0u;
-  }
+#pragma unroll 1
+  for (int b = lane; b < n_seqs; b += 32) s += sm.pref[b] > j ? sm.pref[b] - j : 0u;
   return __reduce_add_sync(0xffffffffu, s);
 }
 
-__device__ __forceinline__ bool prompt_job(const TileParams& p, const Smem& sm, uint32_t id, int lane, Job& jb) {
+__device__ __forceinline__ bool prompt_job(const TileParams& p, const Smem& sm, uint32_t id, uint32_t total, uint32_t most,
+                                           int lane, Job& jb) {
   const uint32_t rank = id / (uint32_t)p.Hkv;
-  uint32_t most = 0;
-  for (int b = lane; b < p.n_seqs; b += 32) most = max(most, sm.pref[b]);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (rank >= blocks_from(sm, p.n_seqs, 0, lane)) return false;
-  uint32_t lo = 0, hi = most;            // blocks_from(lo) > rank >= blocks_from(hi)
-  while (hi - lo > 1) {
-    const uint32_t mid = (lo + hi) >> 1;
-    if (blocks_from(sm, p.n_seqs, mid, lane) > rank) lo = mid;
-    else hi = mid;
+  if (rank >= total) return false;
+  // the block index: blocks_from(lo) > rank >= blocks_from(hi) = behind
+  uint32_t lo = 0, hi = most, behind = 0;
+  if (p.n_seqs == 1) {
+    lo = total - 1 - rank;
+    behind = rank;
+  } else {
+#pragma unroll 1
+    while (hi - lo > 1) {
+      const uint32_t mid = (lo + hi) >> 1, f = blocks_from(sm, p.n_seqs, mid, lane);
+      if (f > rank) lo = mid;
+      else hi = mid, behind = f;
+    }
   }
-  uint32_t k = rank - blocks_from(sm, p.n_seqs, lo + 1, lane);
+  uint32_t k = rank - behind;            // the k-th of the sequences that have this block
   int b = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
     const uint32_t here = __ballot_sync(0xffffffffu, b0 + lane < p.n_seqs && sm.pref[b0 + lane] > lo);
     const uint32_t cnt = __popc(here);
-    if (k < cnt) {                       // the k-th of them
+    if (k < cnt) {
       const bool it = ((here >> lane) & 1u) && __popc(here & ((1u << lane) - 1u)) == (int)k;
       b = b0 + __ffs((int)__ballot_sync(0xffffffffu, it)) - 1;
       break;
@@ -212,11 +217,12 @@ __device__ __forceinline__ bool tree_job(const TileParams& p, const Smem& sm, ui
   return true;
 }
 
-// Walks the CTA's jobs; every warp walks them by itself.
+// Walks the CTA's units; the planning warp's.
 template <bool TREE>
 struct Walk {
-  uint32_t at, begin, end, turn;
-  __device__ Walk(const TileParams& p, const Smem& sm) {
+  uint32_t at = 0, begin = 0, end = 0;   // tree: the CTA's run of tiles
+  uint32_t total = 0, most = 0, turn = 0;  // prompt: blocks of all sequences, and of the longest
+  __device__ Walk(const TileParams& p, const Smem& sm, int lane) {
     if (TREE) {
       const uint32_t W = sm.pref[p.n_seqs];
       const uint32_t share = (W + gridDim.x - 1) / gridDim.x;
@@ -224,9 +230,14 @@ struct Walk {
       end = min(W, begin + share);
       at = begin;
     } else {
-      at = begin = end = 0;
+#pragma unroll 1
+      for (int b = lane; b < p.n_seqs; b += 32) {
+        total += sm.pref[b];
+        most = max(most, sm.pref[b]);
+      }
+      total = __reduce_add_sync(0xffffffffu, total);
+      most = __reduce_max_sync(0xffffffffu, most);
     }
-    turn = 0;
   }
   __device__ bool next(const TileParams& p, const Smem& sm, int lane, Job& j) {
     if (TREE) return tree_job(p, sm, at, begin, end, j);
@@ -234,7 +245,7 @@ struct Walk {
     // longest of every turn
     const uint32_t id = turn * gridDim.x + ((turn & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     ++turn;
-    return prompt_job(p, sm, id, lane, j);
+    return prompt_job(p, sm, id, total, most, lane, j);
   }
 };
 
@@ -438,7 +449,7 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   if (warp >= kWarpMma) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kWarpPlan) {
-    Walk<TREE> walk(p, sm);
+    Walk<TREE> walk(p, sm, lane);
     Job jb;
     for (uint32_t n = 0; ok; ++n) {
       const bool more = walk.next(p, sm, lane, jb);
