@@ -4,16 +4,16 @@
 // its cluster (a contiguous segment per CTA), and every later pass runs from there.
 //
 //   1. the maximum (and for a greedy row its lowest index)
-//   2. one pass for the mass of all weights (where top-p or an unfiltered draw needs it), and for a
-//      histogram of every eighth value over the distance d = (max - l) / T
-//   3. with a filter on: the distance within which the sample tells of some 700 values; those values (at
-//      most 1024) go to CTA 0 in index order, which finds the cut by count and by mass (16 thresholds a
-//      round, one a warp), drops by min-p and draws, while the other CTAs leave
-//   4. where those do not reach the cut (flat or wide filters): a histogram over d in 1024 bins of 1/32,
-//      counts and masses, gives the bin of the cut, whose values CTA 0 sorts; a fuller bin is cut again
-//      by the bits of the values, and one of equal values by their index
-//   5. without a list: the masses of the survivors, a prefix over warps and CTAs, and the element at
-//      u * mass
+//   2. for top-k and top-p a histogram of every fourth value over the distance d = (max - l) / T
+//   3. with top-k or top-p: the sample tells about how far the cut lies.  Exact counts and masses within
+//      two distances around it (again with nearer ones where they miss it) leave a window of at most 1024
+//      values, which go to CTA 0 in index order; it finds the last one kept (16 thresholds a round, one a
+//      warp).  Where the window begins at the maximum CTA 0 drops by min-p and draws, and the others leave.
+//   4. else the masses of the survivors, a prefix over warps and CTAs, and the element at u * mass
+//   5. where no window is found (many equal values, masked or extreme rows, top-p of a large top-k): a
+//      histogram over d in 1024 bins of 1/32, counts and masses, gives the bin of the cut, whose values
+//      CTA 0 sorts; a fuller bin is cut again by the bits of the values, and one of equal values by
+//      their index
 //
 // Weights e^-d are computed in fp64 (table of 2^(j/64) and a Taylor polynomial of degree 4, relative
 // error below 5e-14) and held as whole multiples of 2^-43 of the largest weight: sums of whole numbers do not
@@ -28,6 +28,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tc5.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -42,8 +43,8 @@ constexpr int kList = 1024;
 constexpr int kSeg = 5120;               // values of a CTA above which the cluster grows
 constexpr int kFrac = 43;                // weights are multiples of 2^-43
 constexpr int kCoarse = 128;              // bins of 1/8 of the sampled histogram
-constexpr int kWant = 700;               // listed values aimed at
-constexpr float kNear = 6.f;             // distance from which on a total mass is summed in fp32
+constexpr int kWant = 700;               // values aimed at in a window
+constexpr float kNear = 3.f;             // distance from which on masses that place a cut are summed in fp32
 
 struct SampleParams {
   const float* logits;
@@ -61,17 +62,23 @@ struct SampleParams {
 struct Exchange {
   unsigned long long a, b;
   uint32_t c, d;
+  unsigned long long m;
 };
 
 struct Shared {
   double pow64[64];                      // 2^(j/64)
-  uint32_t coarse[kCoarse];
+  uint32_t coarse[kCoarse];              // sampled values by distance
+  uint32_t coarse_w[kCoarse];            // and their masses, multiples of 2^-18
+  float aim[2];
+  uint32_t beyond_w;                     // mass of the sampled ones behind the last bin
   Exchange ex[2];
   unsigned long long w64[kWarps];
   uint32_t w32[kWarps];
   uint32_t wk[kWarps];
+  Exchange wx[kWarps];
   Exchange found;
   uint32_t n_list;
+  unsigned long long list_mass;
 };
 
 // (ln 2 / 64)^i / i!: 2^(r/64) = sum of these times r^i; |r| <= 1/2, so the next term is below 4e-14
@@ -178,63 +185,90 @@ struct Cut {
   int at;
 };
 
-  // CTA 0: the last element of the shortest prefix (largest first, ties by place) of the m listed values
-  // whose count or mass is >= target, and the mass of that prefix.  Every round, each warp takes one
-  // of 16 thresholds of the range that is left.
-  struct CutMass {
+// CTA 0: the last element of the shortest prefix (largest first, ties by place) of the m listed values (key,
+// place and mass arrays) whose count or mass is >= target, and the mass of that prefix: by 8 bits of the
+// keys' range at a time, then by index among equals.  Every thread has two of the values.
+struct CutMass {
   Cut cut;
   unsigned long long mass;
 };
 __device__ __noinline__ CutMass cut_list(Shared& sm, const uint32_t* key, int m, bool by_count, unsigned long long target) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t* place = key + kList;
-    const unsigned long long* W = reinterpret_cast<const unsigned long long*>(key + 2 * kList);
-    uint32_t a = 0xffffffffu, b = 0;
-    for (int i = lane; i < m; i += 32) a = min(a, key[i]), b = max(b, key[i]);
-    uint32_t lo = __reduce_min_sync(0xffffffffu, a), hi = __reduce_max_sync(0xffffffffu, b) + 1u;
-    // sum(key >= lo) reaches the target, sum(key >= hi) does not
+  const unsigned long long* W = reinterpret_cast<const unsigned long long*>(key + 2 * kList);
+  uint32_t* lo = const_cast<uint32_t*>(key) + 4 * kList;         // [256] low and [256] high words
+  uint32_t* hi = lo + 256;
+  const int i = 2 * tid;
+  const bool in0 = i < m, in1 = i + 1 < m;
+  const uint32_t k0 = in0 ? key[i] : 0u, k1 = in1 ? key[i + 1] : 0u;
+  const unsigned long long w0 = in0 ? W[i] : 0ull, w1 = in1 ? W[i + 1] : 0ull;
+  uint32_t top = __reduce_max_sync(0xffffffffu, max(k0, k1));
+  uint32_t bot = __reduce_min_sync(0xffffffffu, min(in0 ? k0 : 0xffffffffu, in1 ? k1 : 0xffffffffu));
+  __syncthreads();
+  if (lane == 0) sm.w32[warp] = top, sm.wk[warp] = bot;
+  __syncthreads();
+  top = __reduce_max_sync(0xffffffffu, lane < kWarps ? sm.w32[lane] : 0u);
+  bot = __reduce_min_sync(0xffffffffu, lane < kWarps ? sm.wk[lane] : 0xffffffffu);
+  unsigned long long above = 0;          // count or mass of the keys above `top`
+  int shift = 0;
+  while (((top - bot) >> shift) >= 256u) shift += 8;
 #pragma unroll 1
-    while (hi - lo > 1u) {
-      const uint32_t step = (uint32_t)(((unsigned long long)(hi - lo) + kWarps) / (kWarps + 1));
-      const uint32_t mine = lo + step * (uint32_t)(warp + 1);
-      unsigned long long f = 0;
-#pragma unroll 4
-      for (int i = lane; i < m; i += 32)
-        if (key[i] >= mine) f += by_count ? 1ull : W[i];
-      f = warp_sum(f);
-      __syncthreads();
-      if (lane == 0) sm.w32[warp] = mine < hi && mine > lo && f >= target;
-      __syncthreads();
-      const uint32_t ok = __ballot_sync(0xffffffffu, lane < kWarps && sm.w32[lane]);
-      const int n_ok = __popc(ok);       // thresholds rise with the warp: the first n_ok hold
-      const uint32_t base = lo;
-      lo = base + step * (uint32_t)n_ok;
-      hi = min(hi, base + step * (uint32_t)(n_ok + 1));
-    }
-    // values equal to lo, in index order: how many of them, and the last one's place (every warp by itself)
-    unsigned long long above = 0, mass = 0, one = 0;
-    for (int i = lane; i < m; i += 32) {
-      if (key[i] > lo) above += by_count ? 1ull : W[i], mass += W[i];
-      if (key[i] == lo) one = W[i];
-    }
-    above = warp_sum(above);
-    mass = warp_sum(mass);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) one = max(one, __shfl_xor_sync(0xffffffffu, one, o));
-    const unsigned long long need = max(1ull, by_count ? target - above : (target - above + one - 1) / max(1ull, one));
-    unsigned long long seen = 0;
-    int at = 0x7fffffff;
-    for (int i0 = 0; i0 < m; i0 += 32) {
-      const uint32_t here = __ballot_sync(0xffffffffu, i0 + lane < m && key[i0 + lane] == lo);
-      if (seen + __popc(here) >= need) {
-        const bool it = ((here >> lane) & 1u) && seen + __popc(here & ((1u << lane) - 1u)) + 1 == need;
-        at = (int)place[i0 + __ffs((int)__ballot_sync(0xffffffffu, it)) - 1];
-        break;
+  while (true) {
+    lo[tid] = 0;                         // both arrays: kT = 512
+    __syncthreads();
+    auto put = [&](uint32_t k, unsigned long long w, bool in) {
+      if (!in || k > top || k < bot) return;
+      const uint32_t b = (top - k) >> shift;
+      if (by_count) {
+        atomicAdd(&lo[b], 1u);
+      } else {
+        const uint32_t low = (uint32_t)w, old = atomicAdd(&lo[b], low);
+        const uint32_t up = (uint32_t)(w >> 32) + (old + low < old ? 1u : 0u);
+        if (up) atomicAdd(&hi[b], up);
       }
-      seen += __popc(here);
-    }
-    return {{lo, at}, mass + need * one};
+    };
+    put(k0, w0, in0);
+    put(k1, w1, in1);
+    __syncthreads();
+    // each of 8 warps scans 32 bins; the bin where the running sum reaches the target
+    const unsigned long long v = tid < 256 ? (unsigned long long)lo[tid] + ((unsigned long long)hi[tid] << 32) : 0ull;
+    unsigned long long run = warp_scan(v, lane);
+    if (lane == 31) sm.w64[warp] = run;
+    __syncthreads();
+    run += above + warp_sum(lane < warp ? sm.w64[lane] : 0ull);
+    if (tid < 256 && run - v < target && run >= target) sm.found = {run - v, v, (uint32_t)tid, 0};
+    __syncthreads();
+    const Exchange f = sm.found;
+    above = f.a;
+    top -= f.c << shift;
+    bot = shift ? max(bot, top - ((1u << shift) - 1u)) : top;
+    if (shift == 0) break;
+    shift -= 8;
   }
+  // values equal to `top`: of those the first `need` in index order; and the mass above them
+  unsigned long long mass = (k0 > top ? w0 : 0ull) + (k1 > top ? w1 : 0ull);
+  unsigned long long one = in0 && k0 == top ? w0 : in1 && k1 == top ? w1 : 0ull;
+  const bool e0 = in0 && k0 == top, e1 = in1 && k1 == top;
+  const uint32_t b0 = __ballot_sync(0xffffffffu, e0), b1 = __ballot_sync(0xffffffffu, e1);
+  mass = warp_sum(mass);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) one = max(one, __shfl_xor_sync(0xffffffffu, one, o));
+  __syncthreads();
+  if (lane == 0) sm.wx[warp] = {mass, one, (uint32_t)(__popc(b0) + __popc(b1)), 0};
+  __syncthreads();
+  const Exchange v = lane < kWarps ? sm.wx[lane] : Exchange{};
+  mass = warp_sum(v.a);
+  one = v.b;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) one = max(one, __shfl_xor_sync(0xffffffffu, one, o));
+  const uint32_t need = (uint32_t)max(1ull, by_count ? target - above : (target - above + one - 1) / max(1ull, one));
+  const uint32_t low = (1u << lane) - 1u;
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? v.c : 0u) + __popc(b0 & low) + __popc(b1 & low);
+  if (e0 && before + 1 == need) sm.found.d = place[i];
+  if (e1 && before + e0 + 1 == need) sm.found.d = place[i + 1];
+  __syncthreads();
+  return {{top, (int)sm.found.d}, mass + need * one};
+}
 
 struct Row {                             // a CTA's view of its row
   Shared& sm;
@@ -268,38 +302,29 @@ struct Row {                             // a CTA's view of its row
 
   __device__ float distance(float l) const { return (lmax - l) * inv_t; }
 
-  // Mass of this warp's values: all in fp64, or, `rough`, those beyond kNear in fp32 (in a fixed order).
-  // The rough one serves as top-p's total: beyond kNear a weight is below 2^-8.6, and the relative error
-  // of their sum (2^-22 a weight, averaged over thousands) is far below what moves a cut.
-  __device__ unsigned long long warp_mass(bool rough) const {
-    const int a = min(n, warp * per), e = min(n, a + per);
-    unsigned long long m = 0;
-    double w;
-    if (!rough) {
-#pragma unroll 4
-      for (int i = a + lane; i < e; i += 32) m += weight(sm, x[i], dmax, s, &w);
-    } else {
-      const float c = inv_t * 1.4426950408889634f;
-      float far = 0.f;
-#pragma unroll 4
-      for (int i = a + lane; i < e; i += 32) {
-        const float l = x[i];
-        if (distance(l) < kNear) m += weight(sm, l, dmax, s, &w);
-        else far += exp2f((l - lmax) * c);
-      }
-      if (far == far) m += (unsigned long long)__double2ll_rn((double)far * (double)(1ll << kFrac));
-    }
-    return warp_sum(m);
+  // Four values 32 apart (-inf behind e).  Weights are made four abreast, since one alone is a chain of a
+  // dozen fp64 operations.
+  __device__ void load4(int i, int e, float* l) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) l[j] = i + 32 * j < e ? x[i + 32 * j] : -INFINITY;
   }
-
-  // Histogram of every eighth 32 values into the CTA's coarse bins.
+  // Every fourth 32 values, and their masses, by distance.
   __device__ void sample_distances() {
     const int a = min(n, warp * per), e = min(n, a + per);
+    uint32_t beyond = 0;
 #pragma unroll 1
-    for (int i = a + lane; i < e; i += 256) {
-      const float d = distance(x[i]);
-      if (d < kCoarse * 0.125f) atomicAdd(&sm.coarse[(int)(d * 8.f)], 1u);
+    for (int i = a + lane; i < e; i += 128) {
+      const float l = x[i], d = distance(l);
+      const uint32_t w = (uint32_t)(exp2_approx(d * -1.4426950408889634f) * 262144.f);
+      if (d < kCoarse * 0.125f) {
+        atomicAdd(&sm.coarse[(int)(d * 8.f)], 1u);
+        if (w) atomicAdd(&sm.coarse_w[(int)(d * 8.f)], w);
+      } else {
+        beyond += w;
+      }
     }
+    beyond = __reduce_add_sync(0xffffffffu, beyond);
+    if (lane == 0 && beyond) atomicAdd(&sm.beyond_w, beyond);
   }
 
   __device__ int bin0(float l) const { return min(kBins - 1, (int)((lmax - l) * inv_t * 32.f)); }
@@ -423,61 +448,139 @@ struct Row {                             // a CTA's view of its row
     return at;
   }
 
-  // Number and mass of this warp's values nearer than `far`.
-  __device__ uint32_t near_count(float far, unsigned long long* mass) const {
+  // Numbers, and where asked masses, of all values nearer than d1 and than d2 (>= d1), over the cluster: a, c
+  // and b, d of the result; m the mass of all.  (Each warp's stay in sm.wx, each CTA's in buffer *t.)
+  // These masses place a cut: those beyond kNear are summed in fp32 (in a fixed order; below 0.05 of the
+  // largest weight, 2^-22 of error a weight, averaged over thousands of them).  A draw's own masses are
+  // exact.
+  __device__ Exchange within(float d1, float d2, bool mass, int* t) {
     const int a = min(n, warp * per), e = min(n, a + per);
-    uint32_t c = 0;
-    unsigned long long m = 0;
-#pragma unroll 4
-    for (int i = a + lane; i < e; i += 32) {
-      const float l = x[i];
-      if (distance(l) < far) {
+    Exchange v = {};
+    float f1 = 0.f, f2 = 0.f, f = 0.f;
+#pragma unroll 1
+    for (int i = a + lane; i - lane < e; i += 128) {
+      float l[4], d[4];
+      bool close = false;
+      load4(i, e, l);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[j] = distance(l[j]);
+        v.c += d[j] < d1;
+        v.d += d[j] < d2;
+        close |= d[j] < kNear;
+      }
+      if (!mass) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float w = exp2_approx(d[j] * -1.4426950408889634f);
+        if (!(d[j] >= kNear)) w = 0.f;
+        f += w;
+        if (d[j] < d1) f1 += w;
+        if (d[j] < d2) f2 += w;
+      }
+      if (__any_sync(0xffffffffu, close)) {
+        unsigned long long W[4];
         double w;
-        ++c;
-        m += weight(sm, l, dmax, s, &w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) W[j] = weight(sm, l[j], dmax, s, &w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (!(d[j] < kNear)) continue;
+          v.m += W[j];
+          if (d[j] < d1) v.a += W[j];
+          if (d[j] < d2) v.b += W[j];
+        }
       }
     }
-    *mass = warp_sum(m);
+    const double one = (double)(1ll << kFrac);
+    v = {warp_sum(v.a + (unsigned long long)__double2ll_rn((double)f1 * one)),
+         warp_sum(v.b + (unsigned long long)__double2ll_rn((double)f2 * one)), __reduce_add_sync(0xffffffffu, v.c),
+         __reduce_add_sync(0xffffffffu, v.d), warp_sum(v.m + (unsigned long long)__double2ll_rn((double)f * one))};
+    __syncthreads();
+    if (lane == 0) sm.wx[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+      v = lane < kWarps ? sm.wx[lane] : Exchange{};
+      v = {warp_sum(v.a), warp_sum(v.b), __reduce_add_sync(0xffffffffu, v.c), __reduce_add_sync(0xffffffffu, v.d), warp_sum(v.m)};
+    }
+    *t = exchange(v);
+    v = lane < C ? remote(lane, *t) : Exchange{};
+    return {warp_sum(v.a), warp_sum(v.b), __reduce_add_sync(0xffffffffu, v.c), __reduce_add_sync(0xffffffffu, v.d), warp_sum(v.m)};
+  }
+
+  // Number of this warp's values in [near, far).
+  __device__ uint32_t window_count(float near, float far) const {
+    const int a = min(n, warp * per), e = min(n, a + per);
+    uint32_t c = 0;
+#pragma unroll 4
+    for (int i = a + lane; i < e; i += 32) {
+      const float d = distance(x[i]);
+      c += d >= near && d < far;
+    }
     return __reduce_add_sync(0xffffffffu, c);
   }
 
-  // This warp's `c` values nearer than `far` to place `at` on of CTA 0's key and place arrays, in index order.
-  __device__ void gather(float far, uint32_t at, uint32_t c) {
+  // This warp's `c` values in [near, far) to place `at` on of CTA 0's key and place arrays, in index order.
+  __device__ void gather(float near, float far, uint32_t at, uint32_t c) {
     uint32_t* key = cg::this_cluster().map_shared_rank(cnt, 0);
     uint32_t* place = key + kList;
     const int a = min(n, warp * per), e = min(n, a + per);
     const uint32_t stop = at + c;
-#pragma unroll 1
-    for (int i0 = a; i0 < e && at < stop; i0 += 32) {
-      const int i = i0 + lane;
-      const float l = i < e ? x[i] : -INFINITY;
-      const bool in = i < e && distance(l) < far;
-      const uint32_t here = __ballot_sync(0xffffffffu, in);
-      const uint32_t to = at + __popc(here & ((1u << lane) - 1u));
-      if (in && to < (uint32_t)kList) key[to] = key_of(l), place[to] = (uint32_t)(e0 + i);
-      at += __popc(here);
+    for (int i = a + lane; i - lane < e && at < stop; i += 128) {
+      float l[4];
+      uint32_t here[4];
+      load4(i, e, l);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float d = distance(l[j]);
+        here[j] = __ballot_sync(0xffffffffu, d >= near && d < far && i + 32 * j < e);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t to = at + __popc(here[j] & ((1u << lane) - 1u));
+        if (((here[j] >> lane) & 1u) && to < (uint32_t)kList) key[to] = key_of(l[j]), place[to] = (uint32_t)(e0 + i + 32 * j);
+        at += __popc(here[j]);
+      }
     }
   }
 
-  // CTA 0 draws from the m listed values, which hold every cut (`mass`: top-p's total without top-k).
-  __device__ void draw_list(int m, int kk, float tp, float mp, unsigned long long mass, float u, int* token, float* prob) {
-    const bool by_p = tp < 1.f;
-    const uint32_t* key = cnt;
-    const uint32_t* place = cnt + kList;
+  // CTA 0: the masses of the m listed values, and in sm.list_mass their sum; bit j of the result: this thread's
+  // j-th is below `mpd`.
+  __device__ uint32_t list_weights(int m, double mpd) {
     unsigned long long* W = reinterpret_cast<unsigned long long*>(cnt + 2 * kList);
-    const double mpd = mp > 0.f ? fmin((double)mp, 1.0) : 0.0;
-    uint32_t drop = 0;                     // bit j: this thread's j-th value is below min_p
+    uint32_t drop = 0;
+    unsigned long long all = 0;
 #pragma unroll 1
     for (int j = 0; j < 2; ++j) {
       const int i = 2 * tid + j;
       if (i < m) {
         double w;
-        const unsigned long long v = weight(sm, of_key(key[i]), dmax, s, &w);
+        const unsigned long long v = weight(sm, of_key(cnt[i]), dmax, s, &w);
         W[i] = v;
+        all += v;
         if (w < mpd) drop |= 1u << j;
       }
     }
+    all = warp_sum(all);
     __syncthreads();
+    if (lane == 0) sm.w64[warp] = all;
+    __syncthreads();
+    all = warp_sum(lane < kWarps ? sm.w64[lane] : 0ull);
+    if (tid == 0) sm.list_mass = all;
+    __syncthreads();
+    return drop;
+  }
+
+  // CTA 0 draws from the m listed values, which hold every cut (`mass`: top-p's total without top-k; `whole`: they
+  // are the row's all).
+  __device__ void draw_list(int m, bool whole, int kk, float tp, float mp, unsigned long long mass, float u, int* token,
+                            float* prob) {
+    const bool by_p = tp < 1.f;
+    const uint32_t* key = cnt;
+    const uint32_t* place = cnt + kList;
+    const unsigned long long* W = reinterpret_cast<const unsigned long long*>(cnt + 2 * kList);
+    const uint32_t drop = list_weights(m, mp > 0.f ? fmin((double)mp, 1.0) : 0.0);
+    if (whole) mass = sm.list_mass;
     Cut cut = {0, 0x7fffffff};
     if (kk > 0) {
       const CutMass c = cut_list(sm, cnt, m, true, (unsigned long long)kk);
@@ -487,7 +590,7 @@ struct Row {                             // a CTA's view of its row
     if (by_p) {
       const double want = tp > 0.f ? ceil((double)tp * (double)mass) : 1.0;
       const unsigned long long target = max(1ull, min((unsigned long long)want, mass));
-      cut = cut_list(sm, cnt, m, false, target).cut;
+      cut = cut_list(sm, cnt, m, false, min(target, sm.list_mass)).cut;   // (the list's own mass is exact)
     }
     // the survivors' masses in index order
     unsigned long long w0 = 0, w1 = 0;
@@ -600,15 +703,13 @@ struct Row {                             // a CTA's view of its row
   }
 };
 
-// A row whose cut the list does not reach, or without a filter: from the masses of all values.
-__device__ __noinline__ void general(const SampleParams& p, Row R, int row, int mis, int kk, float tp, float mp, float u,
-                                     unsigned long long mass, unsigned long long mine) {
+// The last element kept by top-k, then top-p, of any row.
+__device__ __noinline__ Cut general(Row R, int vocab, int kk, float tp) {
   Shared& sm = R.sm;
-  float* const x = R.x;
-  const int n = R.n, e0 = R.e0, tid = R.tid, lane = R.lane, warp = R.warp, rank = R.rank, C = R.C, per = R.per;
-  const bool by_k = kk > 0 && kk < p.vocab, by_p = tp < 1.f, plain = !by_k && !by_p && !(mp > 0.f);
+  const int tid = R.tid, lane = R.lane, warp = R.warp;
+  const bool by_k = kk > 0 && kk < vocab, by_p = tp < 1.f;
+  unsigned long long mass = 0;
   int t;
-  // ---- top-k, then top-p: the last element kept
   Cut cut = {0, 0x7fffffff};
   bool fresh = false;
   unsigned long long unused;
@@ -640,55 +741,7 @@ __device__ __noinline__ void general(const SampleParams& p, Row R, int row, int 
     const unsigned long long target = max(1ull, min((unsigned long long)want, mass));
     cut = R.search(false, target, true, fresh, &unused);
   }
-  // ---- masses of the survivors, warp by warp in index order
-  const double mpd = mp > 0.f ? fmin((double)mp, 1.0) : 0.0;
-  auto kept = [&](int i) -> unsigned long long {
-    const float l = x[i];
-    const uint32_t k = key_of(l);
-    if (k < cut.key || k == kMasked || (k == cut.key && e0 + i > cut.at)) return 0;
-    double w;
-    const unsigned long long W = weight(sm, l, R.dmax, R.s, &w);
-    return w >= mpd ? W : 0ull;
-  };
-  const int a = min(n, warp * per), e = min(n, a + per);
-  unsigned long long m = mine;           // without a filter the first pass has it
-  if (!plain) {
-    m = 0;
-#pragma unroll 4
-    for (int i = a + lane; i < e; i += 32) m += kept(i);
-    m = warp_sum(m);
-  }
-  __syncthreads();
-  if (lane == 0) sm.w64[warp] = m;
-  __syncthreads();
-  unsigned long long before = 0, here = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sm.w64[w];
-    here += sm.w64[w];
-  }
-  t = R.exchange({here, 0, 0, 0});
-  const unsigned long long theirs = lane < C ? R.remote(lane, t).a : 0ull;
-  before += warp_sum(lane < rank ? theirs : 0ull);
-  const unsigned long long total = warp_sum(theirs);
-  const unsigned long long want = min((unsigned long long)((double)u * (double)total), total - 1);
-  if (before <= want && want < before + m) {             // one warp of the cluster
-    // contiguous parts of the warp's values, one for each lane
-    const int part = per / 32, a2 = min(e, a + lane * part), e2 = min(e, a2 + part);
-    unsigned long long w = 0;
-    for (int i = a2; i < e2; ++i) w += kept(i);
-    unsigned long long run = before + warp_scan(w, lane) - w;
-    if (run <= want && want < run + w)
-      for (int i = a2; i < e2; ++i) {
-        const unsigned long long W = kept(i);
-        if (want < run + W) {
-          p.token[row] = e0 + i - mis;
-          if (p.prob) p.prob[row] = (float)((double)W / (double)total);
-          break;
-        }
-        run += W;
-      }
-  }
-  cg::this_cluster().sync();             // no CTA leaves while another may read its shared memory
+  return cut;
 }
 
 __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
@@ -701,7 +754,8 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   float* x = reinterpret_cast<float*>(dyn);
   uint32_t* cnt = reinterpret_cast<uint32_t*>(x + p.seg);
   if (tid < 64) sm.pow64[tid] = exp2((double)tid / 64.0);
-  if (tid < kCoarse) sm.coarse[tid] = 0;
+  if (tid < kCoarse) sm.coarse[tid] = sm.coarse_w[tid] = 0;
+  if (tid == 0) sm.beyond_w = 0;
 
   // ---- the row into shared memory.  Places are counted from the 16-byte boundary at or below
   // the row's first value, so all inner loads are 16 bytes wide.
@@ -781,69 +835,230 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   R.dmax = (double)R.lmax;
   R.s = 92.332482616893656769 / (double)T;              // 64 log2(e) / T
   const bool by_k = kk > 0 && kk < p.vocab, by_p = tp < 1.f, by_m = mp > 0.f;
-  const bool plain = !by_k && !by_p && !by_m, total = plain || (by_p && !by_k);
-  unsigned long long mass = 0;
-  const unsigned long long mine = total ? R.warp_mass(!plain) : 0ull;
-  if (!plain) {
-    // ---- a distance that holds a list's worth of values, from the sample
+  Cut cut = {0, 0x7fffffff};
+  if (by_k || by_p) {
+    // ---- top-k's count or top-p's mass
+    unsigned long long mass = 0;
+    const bool by_mass = !by_k;
     R.sample_distances();
-    __syncthreads();
-    if (lane == 0) sm.w64[warp] = mine;
-    __syncthreads();
-    t = R.exchange({warp_sum(lane < kWarps ? sm.w64[lane] : 0ull), 0, 0, 0});
-    mass = R.sum_a(t);
-    uint32_t c4[4] = {0, 0, 0, 0};       // bins 4 lane .. 4 lane + 3
+    cluster.sync();
+    // ---- about how far that is, and a distance on both sides of it.  Lane by lane 4 bins.
+    float d1, d2;
+    if (warp == 0) {
+      uint32_t c4[4] = {0, 0, 0, 0}, w4[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int r = 0; r < kMaxC; ++r)
-      if (r < C) {
-        const uint4 v = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(sm.coarse, r) + 4 * lane);
-        c4[0] += v.x, c4[1] += v.y, c4[2] += v.z, c4[3] += v.w;
+      for (int r = 0; r < kMaxC; ++r)
+        if (r < C) {
+          const uint4 v = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(sm.coarse, r) + 4 * lane);
+          const uint4 w = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(sm.coarse_w, r) + 4 * lane);
+          c4[0] += v.x, c4[1] += v.y, c4[2] += v.z, c4[3] += v.w;
+          w4[0] += w.x, w4[1] += w.y, w4[2] += w.z, w4[3] += w.w;
+        }
+      // by mass: from the far end, whose many small weights the sample tells well
+      const float beyond = 4.f * (float)__reduce_add_sync(0xffffffffu, lane < C ? *cluster.map_shared_rank(&sm.beyond_w, lane) : 0u);
+      const uint32_t cs = c4[0] + c4[1] + c4[2] + c4[3];
+      const float ws = (float)w4[0] + (float)w4[1] + (float)w4[2] + (float)w4[3];
+      const uint32_t crun = warp_scan(cs, lane) - cs;
+      const float wall = warp_sum(ws), wrun = warp_scan(ws, lane) - ws;
+      float at = 0.f;                    // this lane's part of the distance: whole bins, and a part of one
+      uint32_t c = crun;
+      const float tail = (1.f - tp) * (beyond + 4.f * wall);
+      float w = beyond + 4.f * (wall - wrun);          // mass from this lane's first bin on
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float cb = 4.f * (float)c4[j], wb = 4.f * (float)w4[j];
+        if (by_mass) at += w - wb > tail ? 1.f : w > tail && wb > 0.f ? (w - tail) / wb : 0.f;
+        else at += 4.f * (float)c + cb < (float)kk ? 1.f : 4.f * (float)c < (float)kk && cb > 0.f ? ((float)kk - 4.f * (float)c) / cb : 0.f;
+        c += c4[j];
+        w -= wb;
       }
-    uint32_t run = warp_scan(c4[0] + c4[1] + c4[2] + c4[3], lane) - (c4[0] + c4[1] + c4[2] + c4[3]);
-    int bins = 0;                        // bins whose running number stays within the list
+      const float mid = 0.125f * warp_sum(at);
+      // the sampled density around it, and half a window's width
+      const int bin = min(kCoarse - 1, (int)(mid * 8.f));
+      uint32_t near_c = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      run += c4[j];
-      bins += run * 8u <= (uint32_t)kWant;
+      for (int j = 0; j < 4; ++j) near_c += 4 * lane + j >= bin - 1 && 4 * lane + j <= bin + 1 ? c4[j] : 0u;
+      near_c = __reduce_add_sync(0xffffffffu, near_c);
+      const float half = fminf(1.f, (kWant / 2) * 0.375f / (4.f * (float)max(1u, near_c)));
+      d1 = mid - half;
+      d2 = mid + half;
+      uint32_t below = 0;                // sampled values nearer than d2
+#pragma unroll
+      for (int j = 0; j < 4; ++j) below += (float)(4 * lane + j) * 0.125f < d2 ? c4[j] : 0u;
+      if (4u * __reduce_add_sync(0xffffffffu, below) <= (uint32_t)kWant) d1 = 0.f;
+      if (p.vocab <= kList) d1 = 0.f, d2 = INFINITY;
+      if (lane == 0) sm.aim[0] = d1, sm.aim[1] = d2;
     }
-    bins = __reduce_add_sync(0xffffffffu, bins);
-    // rows that fit the list whole need no distance
-    const float far = p.vocab <= kList ? INFINITY : (float)max(bins, 1) * 0.125f;
-    // ---- their exact number and mass, and where each warp's begin
-    unsigned long long near_mass;
-    const uint32_t c = R.near_count(far, &near_mass);
     __syncthreads();
-    if (lane == 0) sm.w32[warp] = c, sm.w64[warp] = near_mass;
-    __syncthreads();
-    const uint32_t cw = lane < kWarps ? sm.w32[lane] : 0u;
-    const int t2 = R.exchange({warp_sum(lane < kWarps ? sm.w64[lane] : 0ull), 0, __reduce_add_sync(0xffffffffu, cw), 0});
-    const uint32_t theirs = lane < C ? R.remote(lane, t2).c : 0u;
-    const uint32_t m = __reduce_add_sync(0xffffffffu, theirs);
-    near_mass = R.sum_a(t2);
-    if (p.vocab <= kList) mass = near_mass;
-    // does the list hold the cut?  (min-p alone: 2^-20 covers the rounding of the distances)
-    bool ok = m > 0 && m <= (uint32_t)kList;
-    if (by_k) ok = ok && m >= (uint32_t)kk;
-    else if (by_p) ok = ok && (double)near_mass >= ceil((double)tp * (double)mass);
-    else ok = ok && -logf(fminf(mp, 1.f)) * (1.f + 0x1p-20f) + 0x1p-20f < far;
-    if (ok) {
-      R.gather(far, __reduce_add_sync(0xffffffffu, lane < rank ? theirs : 0u) + __reduce_add_sync(0xffffffffu, lane < warp ? cw : 0u), c);
-      cluster.sync();                    // CTA 0 has the list; nothing else of the others is read any more
-      if (rank != 0) return;
-      int token = -1;
-      float prob = 0.f;
-      R.draw_list((int)m, by_k ? kk : 0, tp, mp, mass, u, &token, &prob);
-      if (token >= 0) {
-        p.token[row] = token - mis;
-        if (p.prob) p.prob[row] = prob;
+    d1 = sm.aim[0];
+    d2 = sm.aim[1];
+    // ---- a window of at most kList values that holds the cut
+    float near = 0.f, far = INFINITY;    // fewer than the target lie nearer than `near`, enough nearer than `far`
+    unsigned long long near_m = 0, far_m = 0;
+    uint32_t near_c = 0, far_c = 0xffffffffu;
+    unsigned long long target = (unsigned long long)kk;
+    bool ok = false;
+    int at_near = 0, at_far = 0;         // where the window's sides are from: 1, 2: the last distances tried
+#pragma unroll 1
+    for (int turn = 0; turn < 20 && !(by_k && by_p && turn > 1); ++turn) {
+      const Exchange v = R.within(d1, d2, by_mass, &t);
+      if (by_mass) {
+        mass = v.m;
+        target = max(1ull, min(tp > 0.f ? (unsigned long long)ceil((double)tp * (double)mass) : 1ull, mass));
       }
-      return;
+      at_near = at_near ? 3 : 0;
+      at_far = 3;
+      const bool one = by_mass ? v.a >= target : v.c >= target, two = by_mass ? v.b >= target : v.d >= target;
+      if (one) {
+        far = d1, far_c = v.c, far_m = v.a, at_far = 1;
+      } else {
+        near = d1, near_c = v.c, near_m = v.a, at_near = 1;
+        if (two) far = d2, far_c = v.d, far_m = v.b, at_far = 2;
+        else near = d2, near_c = v.d, near_m = v.b, at_near = 2;
+      }
+      // (a window from the maximum on saves the pass over the survivors)
+      if (far_c <= (uint32_t)kList) near = 0.f, near_c = 0, near_m = 0, at_near = 0;
+      ok = far_c != 0xffffffffu && far_c - near_c <= (uint32_t)kList;
+      if (ok) break;
+      if (far_c == 0xffffffffu) {        // none far enough yet
+        if (turn >= 8 || near == INFINITY) break;
+        d1 = near + 0.125f * (float)(1 << turn);
+        d2 = d1 + 0.25f * (float)(1 << turn);
+      } else {
+        // on from the distances just tried, by the density between them; else where a straight line
+        // between the two sides meets the target
+        const float span = far - near;
+        const double v1 = by_mass ? (double)v.a : (double)v.c, v2 = by_mass ? (double)v.b : (double)v.d;
+        float mid = d1 + (d2 - d1) * (float)(((double)target - v1) / (v2 - v1));
+        float half = (d2 - d1) * (float)(kWant / 2) / (float)(v.d - v.c);
+        if (!(v2 > v1 && v.d > v.c && mid > near && mid < far && half < 0.25f * span)) {
+          const double n0 = by_mass ? (double)near_m : (double)near_c, n1 = by_mass ? (double)far_m : (double)far_c;
+          mid = near + span * (float)(((double)target - n0) / (n1 - n0));
+          half = span * fmaxf(0.05f, fminf(0.25f, (kWant / 2) / (float)(far_c - near_c)));
+        }
+        d1 = mid - half > near ? mid - half : near + span * 0.01f;
+        d2 = mid + half < far ? mid + half : far - span * 0.01f;
+        if (!(d1 > near && d2 < far && d1 <= d2)) break;      // the distances are used up: equal values
+      }
+    }
+    if (by_k && by_p) ok = ok && near_c == 0;                 // top-p has to lie in the window too
+    if (ok) {
+      // every warp's and every CTA's number of them: known from the last pass, or counted
+      uint32_t cw, theirs;
+      if (at_near < 3 && at_far < 3) {
+        const Exchange w = lane < kWarps ? sm.wx[lane] : Exchange{}, r = lane < C ? R.remote(lane, t) : Exchange{};
+        cw = (at_far == 1 ? w.c : w.d) - (at_near == 0 ? 0u : at_near == 1 ? w.c : w.d);
+        theirs = (at_far == 1 ? r.c : r.d) - (at_near == 0 ? 0u : at_near == 1 ? r.c : r.d);
+      } else {
+        const uint32_t c1 = R.window_count(near, far);
+        __syncthreads();
+        if (lane == 0) sm.w32[warp] = c1;
+        __syncthreads();
+        cw = lane < kWarps ? sm.w32[lane] : 0u;
+        t = R.exchange({0, 0, __reduce_add_sync(0xffffffffu, cw), 0});
+        theirs = lane < C ? R.remote(lane, t).c : 0u;
+      }
+      const uint32_t c = __shfl_sync(0xffffffffu, cw, warp);
+      const int m = (int)__reduce_add_sync(0xffffffffu, theirs);
+      R.gather(near, far, __reduce_add_sync(0xffffffffu, lane < rank ? theirs : 0u) + __reduce_add_sync(0xffffffffu, lane < warp ? cw : 0u), c);
+      cluster.sync();
+      if (near_c == 0) {
+        // CTA 0 has every candidate; nothing of the other CTAs is read any more
+        if (rank != 0) return;
+        int token = -1;
+        float prob = 0.f;
+        R.draw_list(m, p.vocab <= kList, by_k ? kk : 0, tp, mp, mass, u, &token, &prob);
+        if (token >= 0) {
+          p.token[row] = token - mis;
+          if (p.prob) p.prob[row] = prob;
+        }
+        return;
+      }
+      Exchange got = {};
+      if (rank == 0) {
+        R.list_weights(m, 0.0);
+        const CutMass r = cut_list(sm, R.cnt, m, by_k, by_mass ? min(target - near_m, sm.list_mass) : target - near_c);
+        got = {0, 0, r.cut.key, (uint32_t)r.cut.at};
+      }
+      t = R.exchange(got);
+      cut = {R.remote(0, t).c, (int)R.remote(0, t).d};
+    } else {
+      cut = general(R, p.vocab, kk, tp);
+      cluster.sync();                    // its last exchange has been read: both buffers are free again
     }
   }
-  general(p, R, row, mis, kk, tp, mp, u, mass, mine);
+  // ---- masses of the survivors, warp by warp in index order
+  const double mpd = by_m ? fmin((double)mp, 1.0) : 0.0;
+  // (a distance that min-p cannot reach; 2^-20 covers the rounding of the distances)
+  const float far = by_m ? -logf(fminf(mp, 1.f)) * (1.f + 0x1p-20f) + 0x1p-20f : INFINITY;
+  const int a = min(n, warp * per), e = min(n, a + per);
+  // the masses of 4 values 32 apart from i on (0 where dropped)
+  auto kept4 = [&](int i, unsigned long long* W) {
+    float l[4];
+    R.load4(i, e, l);
+    bool in[4], any = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t k = key_of(l[j]);
+      in[j] = k != kMasked && (k > cut.key || (k == cut.key && e0 + i + 32 * j <= cut.at)) && !(R.distance(l[j]) > far);
+      any |= in[j];
+      W[j] = 0;
+    }
+    if (!__any_sync(0xffffffffu, any)) return;
+    double w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) W[j] = weight(sm, l[j], R.dmax, R.s, &w[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (!in[j] || w[j] < mpd) W[j] = 0;
+  };
+  unsigned long long m = 0, W[4];
+#pragma unroll 1
+  for (int i = a + lane; i - lane < e; i += 128) {
+    kept4(i, W);
+    m += (W[0] + W[1]) + (W[2] + W[3]);
+  }
+  m = warp_sum(m);
+  __syncthreads();
+  if (lane == 0) sm.w64[warp] = m;
+  __syncthreads();
+  unsigned long long before = 0, here = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sm.w64[w];
+    here += sm.w64[w];
+  }
+  t = R.exchange({here, 0, 0, 0});
+  const unsigned long long theirs = lane < C ? R.remote(lane, t).a : 0ull;
+  before += warp_sum(lane < rank ? theirs : 0ull);
+  const unsigned long long total = warp_sum(theirs);
+  const unsigned long long want = min((unsigned long long)((double)u * (double)total), total - 1);
+  if (before <= want && want < before + m) {             // one warp of the cluster
+    unsigned long long run = before;
+#pragma unroll 1
+    for (int i = a + lane; i - lane < e; i += 128) {
+      kept4(i, W);
+      const unsigned long long all = warp_sum((W[0] + W[1]) + (W[2] + W[3]));
+      if (want >= run + all) {
+        run += all;
+        continue;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const unsigned long long upto = run + warp_scan(W[j], lane);
+        if (upto - W[j] <= want && want < upto) {
+          p.token[row] = e0 + i + 32 * j - mis;
+          if (p.prob) p.prob[row] = (float)((double)W[j] / (double)total);
+        }
+        run = __shfl_sync(0xffffffffu, upto, 31);
+      }
+      break;
+    }
+  }
+  cluster.sync();                        // no CTA leaves while another may read its shared memory
 }
 
 int sample_smem(int seg) { return seg * 4 + 3 * kBins * 4 + kList * 8; }
+static_assert(4 * kList * 4 + 2 * 256 * 4 <= 3 * kBins * 4 + kList * 8 && kT == 512, "the list and its bins lie over the histogram and its list");
 
 }  // namespace
 
