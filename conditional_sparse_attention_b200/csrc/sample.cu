@@ -43,7 +43,7 @@ constexpr int kList = 1024;
 constexpr int kSeg = 5120;               // values of a CTA above which the cluster grows
 constexpr int kFrac = 43;                // weights are multiples of 2^-43
 constexpr int kCoarse = 128;              // bins of 1/8 of the sampled histogram
-constexpr int kWant = 700;               // values aimed at in a window
+constexpr int kWant = 900;               // values aimed at in a window
 constexpr float kNear = 3.f;             // distance from which on masses that place a cut are summed in fp32
 
 struct SampleParams {
@@ -57,13 +57,15 @@ struct SampleParams {
   float* prob;
   int64_t row_stride;
   int vocab, seg;                        // seg: values of a CTA, a multiple of 4
+  int32_t* err;
 };
 
-struct Exchange {
+struct alignas(16) Exchange {
   unsigned long long a, b;
   uint32_t c, d;
   unsigned long long m;
 };
+static_assert(sizeof(Exchange) == 32, "two 16-byte stores");
 
 struct Shared {
   double pow64[64];                      // 2^(j/64)
@@ -71,7 +73,8 @@ struct Shared {
   uint32_t coarse_w[kCoarse];            // and their masses, multiples of 2^-18
   float aim[2];
   uint32_t beyond_w;                     // mass of the sampled ones behind the last bin
-  Exchange ex[2];
+  alignas(16) Exchange ex[2][kMaxC];     // what each CTA told this one, in two buffers used in turn
+  alignas(8) uint64_t told[2];           // and the barriers that count its bytes
   unsigned long long w64[kWarps];
   uint32_t w32[kWarps];
   uint32_t wk[kWarps];
@@ -112,8 +115,15 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 }
 constexpr uint32_t kMasked = 0x007fffffu;               // key of -inf
 
-template <class T>
-__device__ __forceinline__ T warp_sum(T v) {
+// Sum over a warp of values whose sum is below 2^62: three whole-warp reductions of 21 bits and the rest
+// (a tenth of the time of ten shuffles).
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x1fffffu);
+  const uint32_t mid = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 21) & 0x1fffffu);
+  const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 42));
+  return ((unsigned long long)hi << 42) + ((unsigned long long)mid << 21) + lo;
+}
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -270,6 +280,12 @@ __device__ __noinline__ CutMass cut_list(Shared& sm, const uint32_t* key, int m,
   return {{top, (int)sm.found.d}, mass + need * one};
 }
 
+// 16 bytes into another CTA's shared memory, counted on a barrier there.
+__device__ __forceinline__ void store_async16(uint32_t to, uint32_t bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+               ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar) : "memory");
+}
+
 struct Row {                             // a CTA's view of its row
   Shared& sm;
   float* x;                              // its segment
@@ -279,20 +295,36 @@ struct Row {                             // a CTA's view of its row
   unsigned long long* list;              // [kList] (~key, place)
   int e0, n;                             // place of x[0] in the row; values here
   int C, rank, tid, lane, warp;
-  int turn;                              // of the exchange buffers
+  int turn;                              // exchanges so far
   int per;                               // values of a warp's contiguous part
   float lmax;
   float inv_t;
   double s, dmax;                        // 64 log2(e) / T, the maximum
+  int32_t* err;
 
-  __device__ Exchange& remote(int r, int t) { return cg::this_cluster().map_shared_rank(&sm, r)->ex[t]; }
+  __device__ const Exchange& remote(int r, int t) const { return sm.ex[t][r]; }
 
-  // Every CTA's thread 0 gives `mine`; returns after all CTAs' values can be read with remote(r, t).
+  // Every CTA's thread 0 has `mine`; returns the buffer t in which remote(r, t) is CTA r's.  The values
+  // are pushed into every CTA's shared memory, which counts their bytes: one way through the cluster
+  // instead of a barrier and the way there and back.  A CTA that is one exchange ahead writes the other
+  // buffer; it cannot be two ahead, since that needs this one's values of the exchange between.
   __device__ int exchange(const Exchange& mine) {
-    const int t = turn;
-    turn ^= 1;
-    if (tid == 0) sm.ex[t] = mine;
-    cg::this_cluster().sync();
+    const int t = turn & 1, parity = (turn >> 1) & 1;
+    ++turn;
+    if (warp == 0) {
+      const unsigned long long va = __shfl_sync(0xffffffffu, mine.a, 0), vb = __shfl_sync(0xffffffffu, mine.b, 0);
+      const unsigned long long vm = __shfl_sync(0xffffffffu, mine.m, 0);
+      const uint32_t vc = __shfl_sync(0xffffffffu, mine.c, 0), vd = __shfl_sync(0xffffffffu, mine.d, 0);
+      if (lane == 0) mbar_arrive_expect_tx(&sm.told[t], (uint32_t)(C * sizeof(Exchange)));
+      if (lane < C) {
+        const uint32_t to = mapa_shared(smem_u32(&sm.ex[t][rank]), (uint32_t)lane);
+        const uint32_t bar = mapa_shared(smem_u32(&sm.told[t]), (uint32_t)lane);
+        store_async16(to, bar, (uint32_t)va, (uint32_t)(va >> 32), (uint32_t)vb, (uint32_t)(vb >> 32));
+        store_async16(to + 16, bar, vc, vd, (uint32_t)vm, (uint32_t)(vm >> 32));
+      }
+    }
+    // (a wait that gave up is reported; the row's token is then undefined)
+    if (!mbar_wait_bounded(&sm.told[t], parity, 2000000000ull)) atomicOr(err, ODA_DEVERR_WAIT_TIMEOUT);
     return t;
   }
 
@@ -419,7 +451,7 @@ struct Row {                             // a CTA's view of its row
     const int a = min(n, warp * per), e = min(n, a + per);
     uint32_t c = 0;
     for (int i = a + lane; i < e; i += 32) c += key_of(x[i]) == k;
-    c = warp_sum(c);
+    c = __reduce_add_sync(0xffffffffu, c);
     __syncthreads();
     if (lane == 0) sm.w32[warp] = c;
     if (tid == 0) sm.found = {};
@@ -704,7 +736,7 @@ struct Row {                             // a CTA's view of its row
 };
 
 // The last element kept by top-k, then top-p, of any row.
-__device__ __noinline__ Cut general(Row R, int vocab, int kk, float tp) {
+__device__ __noinline__ Cut general(Row R, int vocab, int kk, float tp, int* turn) {
   Shared& sm = R.sm;
   const int tid = R.tid, lane = R.lane, warp = R.warp;
   const bool by_k = kk > 0 && kk < vocab, by_p = tp < 1.f;
@@ -741,6 +773,7 @@ __device__ __noinline__ Cut general(Row R, int vocab, int kk, float tp) {
     const unsigned long long target = max(1ull, min((unsigned long long)want, mass));
     cut = R.search(false, target, true, fresh, &unused);
   }
+  *turn = R.turn;
   return cut;
 }
 
@@ -753,6 +786,12 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float* x = reinterpret_cast<float*>(dyn);
   uint32_t* cnt = reinterpret_cast<uint32_t*>(x + p.seg);
+  if (tid == 0) {
+    mbar_init(&sm.told[0], 1);
+    mbar_init(&sm.told[1], 1);
+    fence_mbar_init();
+  }
+  cluster_arrive();                      // waited for before the first exchange
   if (tid < 64) sm.pow64[tid] = exp2((double)tid / 64.0);
   if (tid < kCoarse) sm.coarse[tid] = sm.coarse_w[tid] = 0;
   if (tid == 0) sm.beyond_w = 0;
@@ -794,7 +833,8 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   best = __reduce_max_sync(0xffffffffu, lane < kWarps ? sm.w32[lane] : 0u);
   const int per = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
   Row R = {sm, x, cnt, cnt + kBins, cnt + 2 * kBins, reinterpret_cast<unsigned long long*>(cnt + 3 * kBins),
-           e0, n, C, rank, tid, lane, warp, 0, per, 0.f, 1.f, 0.0, 0.0};
+           e0, n, C, rank, tid, lane, warp, 0, per, 0.f, 1.f, 0.0, 0.0, p.err};
+  cluster_wait();                        // every CTA's barriers are there
   int t = R.exchange({0, 0, best, 0});
   best = __reduce_max_sync(0xffffffffu, lane < C ? R.remote(lane, t).c : 0u);
   // ---- settings
@@ -821,7 +861,6 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
       p.token[row] = none ? -1 : (int)at - mis;
       if (p.prob) p.prob[row] = none ? 0.f : 1.f;
     }
-    cluster.sync();                      // the exchange above may still be read
     return;
   }
   R.lmax = of_key(best);
@@ -983,8 +1022,9 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
       t = R.exchange(got);
       cut = {R.remote(0, t).c, (int)R.remote(0, t).d};
     } else {
-      cut = general(R, p.vocab, kk, tp);
-      cluster.sync();                    // its last exchange has been read: both buffers are free again
+      int turns;
+      cut = general(R, p.vocab, kk, tp, &turns);
+      R.turn = turns;
     }
   }
   // ---- masses of the survivors, warp by warp in index order
@@ -1054,7 +1094,6 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
       break;
     }
   }
-  cluster.sync();                        // no CTA leaves while another may read its shared memory
 }
 
 int sample_smem(int seg) { return seg * 4 + 3 * kBins * 4 + kList * 8; }
@@ -1082,7 +1121,7 @@ oda_status launch_sample(oda_ctx* ctx, int n_rows, int vocab, int64_t row_stride
   for (const void* q : al)
     if (reinterpret_cast<uintptr_t>(q) & 3) return set_error(ODA_ERR_INVALID_ARG, "sample: buffers must be 4-byte aligned");
   ctx->prev_attention = false;
-  SampleParams p = {logits, temperature, top_k, top_p, min_p, u, token, prob, row_stride, vocab, 0};
+  SampleParams p = {logits, temperature, top_k, top_p, min_p, u, token, prob, row_stride, vocab, 0, ctx->err};
   const int places = vocab + 3;          // the row may start up to 3 places behind a 16-byte boundary
   int C = 1;
   while (C < kMaxC && (places + C - 1) / C > kSeg) C *= 2;
