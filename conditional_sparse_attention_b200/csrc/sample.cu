@@ -4,9 +4,9 @@
 // its cluster (a contiguous segment per CTA), and every later pass runs from there.
 //
 //   1. the maximum (and for a greedy row its lowest index)
-//   2. for top-k and top-p a histogram of every fourth value over the distance d = (max - l) / T
-//   3. with top-k or top-p: the sample tells about how far the cut lies.  Exact counts and masses within
-//      two distances around it (again with nearer ones where they miss it) leave a window of at most 1024
+//   2. for top-k and top-p a histogram over the distance d = (max - l) / T, in 512 bins of 1/32
+//   3. it tells closely how far the cut lies (a bin's weights differ by 3%).  Exact counts and masses within
+//      two distances around that (again with others where they miss it) leave a window of at most 1024
 //      values, which go to CTA 0 in index order; it finds the last one kept (16 thresholds a round, one a
 //      warp).  Where the window begins at the maximum CTA 0 drops by min-p and draws, and the others leave.
 //   4. else the masses of the survivors, a prefix over warps and CTAs, and the element at u * mass
@@ -42,7 +42,8 @@ constexpr int kBins = 1024;
 constexpr int kList = 1024;
 constexpr int kSeg = 5120;               // values of a CTA above which the cluster grows
 constexpr int kFrac = 43;                // weights are multiples of 2^-43
-constexpr int kCoarse = 128;              // bins of 1/8 of the sampled histogram
+constexpr int kCoarse = 512;              // bins of the histogram that aims
+constexpr float kCoarseBins = 32.f;       // bins to a distance of 1
 constexpr int kWant = 900;               // values aimed at in a window
 constexpr float kNear = 3.f;             // distance from which on masses that place a cut are summed in fp32
 
@@ -69,10 +70,9 @@ static_assert(sizeof(Exchange) == 32, "two 16-byte stores");
 
 struct Shared {
   double pow64[64];                      // 2^(j/64)
-  uint32_t coarse[kCoarse];              // sampled values by distance
-  uint32_t coarse_w[kCoarse];            // and their masses, multiples of 2^-18
+  alignas(16) uint32_t coarse[kCoarse];  // values by distance
   float aim[2];
-  uint32_t beyond_w;                     // mass of the sampled ones behind the last bin
+  float wbeyond[kWarps];                 // each warp's mass behind the last bin
   alignas(16) Exchange ex[2][kMaxC];     // what each CTA told this one, in two buffers used in turn
   alignas(8) uint64_t told[2];           // and the barriers that count its bytes
   unsigned long long w64[kWarps];
@@ -340,23 +340,23 @@ struct Row {                             // a CTA's view of its row
 #pragma unroll
     for (int j = 0; j < 4; ++j) l[j] = i + 32 * j < e ? x[i + 32 * j] : -INFINITY;
   }
-  // Every fourth 32 values, and their masses, by distance.
-  __device__ void sample_distances() {
+  // The CTA's values by distance, and the mass of those behind the last bin.
+  __device__ void distances() {
     const int a = min(n, warp * per), e = min(n, a + per);
-    uint32_t beyond = 0;
+    float beyond = 0.f;
 #pragma unroll 1
-    for (int i = a + lane; i < e; i += 128) {
-      const float l = x[i], d = distance(l);
-      const uint32_t w = (uint32_t)(exp2_approx(d * -1.4426950408889634f) * 262144.f);
-      if (d < kCoarse * 0.125f) {
-        atomicAdd(&sm.coarse[(int)(d * 8.f)], 1u);
-        if (w) atomicAdd(&sm.coarse_w[(int)(d * 8.f)], w);
-      } else {
-        beyond += w;
+    for (int i = a + lane; i - lane < e; i += 128) {
+      float l[4];
+      load4(i, e, l);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float d = distance(l[j]), b = d * kCoarseBins;
+        if (b < (float)kCoarse) atomicAdd(&sm.coarse[(int)b], 1u);
+        else beyond += exp2_approx(d * -1.4426950408889634f);
       }
     }
-    beyond = __reduce_add_sync(0xffffffffu, beyond);
-    if (lane == 0 && beyond) atomicAdd(&sm.beyond_w, beyond);
+    beyond = warp_sum(beyond);
+    if (lane == 0) sm.wbeyond[warp] = beyond;
   }
 
   __device__ int bin0(float l) const { return min(kBins - 1, (int)((lmax - l) * inv_t * 32.f)); }
@@ -793,8 +793,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   }
   cluster_arrive();                      // waited for before the first exchange
   if (tid < 64) sm.pow64[tid] = exp2((double)tid / 64.0);
-  if (tid < kCoarse) sm.coarse[tid] = sm.coarse_w[tid] = 0;
-  if (tid == 0) sm.beyond_w = 0;
+  sm.coarse[tid] = 0;                    // kCoarse = kT
 
   // ---- the row into shared memory.  Places are counted from the 16-byte boundary at or below
   // the row's first value, so all inner loads are 16 bytes wide.
@@ -879,52 +878,58 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
     // ---- top-k's count or top-p's mass
     unsigned long long mass = 0;
     const bool by_mass = !by_k;
-    R.sample_distances();
+    R.distances();
     cluster.sync();
-    // ---- about how far that is, and a distance on both sides of it.  Lane by lane 4 bins.
+    // ---- how far that is, to a few values, and a distance on both sides of it.  16 bins a lane.
     float d1, d2;
     if (warp == 0) {
-      uint32_t c4[4] = {0, 0, 0, 0}, w4[4] = {0, 0, 0, 0};
+      constexpr int kPer = kCoarse / 32;
+      uint32_t c[kPer] = {};
 #pragma unroll
       for (int r = 0; r < kMaxC; ++r)
         if (r < C) {
-          const uint4 v = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(sm.coarse, r) + 4 * lane);
-          const uint4 w = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(sm.coarse_w, r) + 4 * lane);
-          c4[0] += v.x, c4[1] += v.y, c4[2] += v.z, c4[3] += v.w;
-          w4[0] += w.x, w4[1] += w.y, w4[2] += w.z, w4[3] += w.w;
-        }
-      // by mass: from the far end, whose many small weights the sample tells well
-      const float beyond = 4.f * (float)__reduce_add_sync(0xffffffffu, lane < C ? *cluster.map_shared_rank(&sm.beyond_w, lane) : 0u);
-      const uint32_t cs = c4[0] + c4[1] + c4[2] + c4[3];
-      const float ws = (float)w4[0] + (float)w4[1] + (float)w4[2] + (float)w4[3];
-      const uint32_t crun = warp_scan(cs, lane) - cs;
-      const float wall = warp_sum(ws), wrun = warp_scan(ws, lane) - ws;
-      float at = 0.f;                    // this lane's part of the distance: whole bins, and a part of one
-      uint32_t c = crun;
-      const float tail = (1.f - tp) * (beyond + 4.f * wall);
-      float w = beyond + 4.f * (wall - wrun);          // mass from this lane's first bin on
+          const uint4* theirs = reinterpret_cast<const uint4*>(cluster.map_shared_rank(sm.coarse, r) + kPer * lane);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float cb = 4.f * (float)c4[j], wb = 4.f * (float)w4[j];
-        if (by_mass) at += w - wb > tail ? 1.f : w > tail && wb > 0.f ? (w - tail) / wb : 0.f;
-        else at += 4.f * (float)c + cb < (float)kk ? 1.f : 4.f * (float)c < (float)kk && cb > 0.f ? ((float)kk - 4.f * (float)c) / cb : 0.f;
-        c += c4[j];
-        w -= wb;
+          for (int j = 0; j < kPer / 4; ++j) {
+            const uint4 v = theirs[j];
+            c[4 * j] += v.x, c[4 * j + 1] += v.y, c[4 * j + 2] += v.z, c[4 * j + 3] += v.w;
+          }
+        }
+      float beyond = 0.f;
+      for (int w = lane; w < C * kWarps; w += 32) beyond += cluster.map_shared_rank(sm.wbeyond, w / kWarps)[w % kWarps];
+      beyond = warp_sum(beyond);
+      // a bin's values at the weight of its middle, top-k: at 1
+      const float w0 = by_mass ? exp2_approx(-1.4426950408889634f / kCoarseBins * ((float)(kPer * lane) + 0.5f)) : 1.f;
+      const float fall = by_mass ? exp2_approx(-1.4426950408889634f / kCoarseBins) : 1.f;
+      float mine = 0.f, w = w0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) mine += w * (float)c[j], w *= fall;
+      // from the far end, where the weights are small: how much lies behind the cut, and bin by bin
+      const float all = warp_sum(mine);
+      const float behind = by_mass ? (1.f - tp) * (all + beyond) - beyond : all - (float)kk;
+      float from = all - (warp_scan(mine, lane) - mine);          // in this lane's first bin and behind
+      float at = 0.f;                    // this lane's part of the distance: whole bins, and a part of one
+      w = w0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const float wb = w * (float)c[j];
+        at += from - wb > behind ? 1.f : from > behind && wb > 0.f ? (from - behind) / wb : 0.f;
+        from -= wb;
+        w *= fall;
       }
-      const float mid = 0.125f * warp_sum(at);
-      // the sampled density around it, and half a window's width
-      const int bin = min(kCoarse - 1, (int)(mid * 8.f));
+      const float mid = warp_sum(at);    // in bins
+      // the values in the three bins around it, and half a window's width
       uint32_t near_c = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) near_c += 4 * lane + j >= bin - 1 && 4 * lane + j <= bin + 1 ? c4[j] : 0u;
+      for (int j = 0; j < kPer; ++j) near_c += fabsf((float)(kPer * lane + j) + 0.5f - mid) < 1.5f ? c[j] : 0u;
       near_c = __reduce_add_sync(0xffffffffu, near_c);
-      const float half = fminf(1.f, (kWant / 2) * 0.375f / (4.f * (float)max(1u, near_c)));
-      d1 = mid - half;
-      d2 = mid + half;
-      uint32_t below = 0;                // sampled values nearer than d2
+      const float half = fminf(kCoarseBins, (float)(kWant / 2) * 3.f / (float)max(1u, near_c));
+      d1 = fmaxf(0.f, mid - half) / kCoarseBins;
+      d2 = (mid + half) / kCoarseBins;
+      uint32_t below = 0;                // values nearer than about d2
 #pragma unroll
-      for (int j = 0; j < 4; ++j) below += (float)(4 * lane + j) * 0.125f < d2 ? c4[j] : 0u;
-      if (4u * __reduce_add_sync(0xffffffffu, below) <= (uint32_t)kWant) d1 = 0.f;
+      for (int j = 0; j < kPer; ++j) below += (float)(kPer * lane + j) < mid + half ? c[j] : 0u;
+      if (__reduce_add_sync(0xffffffffu, below) <= (uint32_t)kList) d1 = 0.f;
       if (p.vocab <= kList) d1 = 0.f, d2 = INFINITY;
       if (lane == 0) sm.aim[0] = d1, sm.aim[1] = d2;
     }
