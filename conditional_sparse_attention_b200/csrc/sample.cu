@@ -71,7 +71,6 @@ static_assert(sizeof(Exchange) == 32, "two 16-byte stores");
 struct Shared {
   double pow64[64];                      // 2^(j/64)
   alignas(16) uint32_t coarse[kCoarse];  // values by distance
-  float aim[2];
   float wbeyond[kWarps];                 // each warp's mass behind the last bin
   alignas(16) Exchange ex[2][kMaxC];     // what each CTA told this one, in two buffers used in turn
   alignas(8) uint64_t told[2];           // and the barriers that count its bytes
@@ -879,63 +878,44 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
     unsigned long long mass = 0;
     const bool by_mass = !by_k;
     R.distances();
+    if (tid < 2) sm.w32[tid] = 0;
     cluster.sync();
-    // ---- how far that is, to a few values, and a distance on both sides of it.  16 bins a lane.
+    // ---- how far that is, to a few values, and a distance on both sides of it.  A bin a thread.
     float d1, d2;
-    if (warp == 0) {
-      constexpr int kPer = kCoarse / 32;
-      uint32_t c[kPer] = {};
+    {
+      uint32_t c = 0;
 #pragma unroll
       for (int r = 0; r < kMaxC; ++r)
-        if (r < C) {
-          const uint4* theirs = reinterpret_cast<const uint4*>(cluster.map_shared_rank(sm.coarse, r) + kPer * lane);
-#pragma unroll
-          for (int j = 0; j < kPer / 4; ++j) {
-            const uint4 v = theirs[j];
-            c[4 * j] += v.x, c[4 * j + 1] += v.y, c[4 * j + 2] += v.z, c[4 * j + 3] += v.w;
-          }
-        }
+        if (r < C) c += cluster.map_shared_rank(sm.coarse, r)[tid];
       float beyond = 0.f;
       for (int w = lane; w < C * kWarps; w += 32) beyond += cluster.map_shared_rank(sm.wbeyond, w / kWarps)[w % kWarps];
       beyond = warp_sum(beyond);
       // a bin's values at the weight of its middle, top-k: at 1
-      const float w0 = by_mass ? exp2_approx(-1.4426950408889634f / kCoarseBins * ((float)(kPer * lane) + 0.5f)) : 1.f;
-      const float fall = by_mass ? exp2_approx(-1.4426950408889634f / kCoarseBins) : 1.f;
-      float mine = 0.f, w = w0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) mine += w * (float)c[j], w *= fall;
-      // from the far end, where the weights are small: how much lies behind the cut, and bin by bin
-      const float all = warp_sum(mine);
+      const float wb = (float)c * (by_mass ? exp2_approx(-1.4426950408889634f / kCoarseBins * ((float)tid + 0.5f)) : 1.f);
+      const float run = warp_scan(wb, lane);
+      __syncthreads();
+      if (lane == 31) sm.wx[warp].a = (unsigned long long)__float_as_uint(run);
+      __syncthreads();
+      const float part = lane < kWarps ? __uint_as_float((uint32_t)sm.wx[lane].a) : 0.f;
+      // from the far end, where the weights are small: how much lies behind the cut, and in this bin and behind
+      const float all = warp_sum(part), from = all - warp_sum(lane < warp ? part : 0.f) - run + wb;
       const float behind = by_mass ? (1.f - tp) * (all + beyond) - beyond : all - (float)kk;
-      float from = all - (warp_scan(mine, lane) - mine);          // in this lane's first bin and behind
-      float at = 0.f;                    // this lane's part of the distance: whole bins, and a part of one
-      w = w0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const float wb = w * (float)c[j];
-        at += from - wb > behind ? 1.f : from > behind && wb > 0.f ? (from - behind) / wb : 0.f;
-        from -= wb;
-        w *= fall;
-      }
-      const float mid = warp_sum(at);    // in bins
-      // the values in the three bins around it, and half a window's width
-      uint32_t near_c = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) near_c += fabsf((float)(kPer * lane + j) + 0.5f - mid) < 1.5f ? c[j] : 0u;
-      near_c = __reduce_add_sync(0xffffffffu, near_c);
-      const float half = fminf(kCoarseBins, (float)(kWant / 2) * 3.f / (float)max(1u, near_c));
-      d1 = fmaxf(0.f, mid - half) / kCoarseBins;
+      const float at = warp_sum(from - wb > behind ? 1.f : from > behind && wb > 0.f ? (from - behind) / wb : 0.f);
+      if (lane == 0) sm.wx[warp].c = __float_as_uint(at);
+      __syncthreads();
+      const float mid = warp_sum(lane < kWarps ? __uint_as_float(sm.wx[lane].c) : 0.f);           // in bins
+      // the values in the three bins around it, and half a window's width; the values nearer than its far end
+      const uint32_t three = __reduce_add_sync(0xffffffffu, fabsf((float)tid + 0.5f - mid) < 1.5f ? c : 0u);
+      if (lane == 0 && three) atomicAdd(&sm.w32[0], three);
+      __syncthreads();
+      const float half = fminf(kCoarseBins, (float)(kWant / 2) * 3.f / (float)max(1u, sm.w32[0]));
+      const uint32_t below = __reduce_add_sync(0xffffffffu, (float)tid < mid + half ? c : 0u);
+      if (lane == 0 && below) atomicAdd(&sm.w32[1], below);
+      __syncthreads();
+      d1 = sm.w32[1] <= (uint32_t)kList ? 0.f : fmaxf(0.f, mid - half) / kCoarseBins;
       d2 = (mid + half) / kCoarseBins;
-      uint32_t below = 0;                // values nearer than about d2
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) below += (float)(kPer * lane + j) < mid + half ? c[j] : 0u;
-      if (__reduce_add_sync(0xffffffffu, below) <= (uint32_t)kList) d1 = 0.f;
       if (p.vocab <= kList) d1 = 0.f, d2 = INFINITY;
-      if (lane == 0) sm.aim[0] = d1, sm.aim[1] = d2;
     }
-    __syncthreads();
-    d1 = sm.aim[0];
-    d2 = sm.aim[1];
     // ---- a window of at most kList values that holds the cut
     float near = 0.f, far = INFINITY;    // fewer than the target lie nearer than `near`, enough nearer than `far`
     unsigned long long near_m = 0, far_m = 0;
@@ -1038,14 +1018,17 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   const float far = by_m ? -logf(fminf(mp, 1.f)) * (1.f + 0x1p-20f) + 0x1p-20f : INFINITY;
   const int a = min(n, warp * per), e = min(n, a + per);
   // the masses of 4 values 32 apart from i on (0 where dropped)
+  const bool cuts = cut.key > kMasked;  // else every unmasked value stays
+  const float edge = cuts ? of_key(cut.key) : -INFINITY;
+  const int edge_at = cuts ? cut.at : -1;
   auto kept4 = [&](int i, unsigned long long* W) {
     float l[4];
     R.load4(i, e, l);
     bool in[4], any = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t k = key_of(l[j]);
-      in[j] = k != kMasked && (k > cut.key || (k == cut.key && e0 + i + 32 * j <= cut.at)) && !(R.distance(l[j]) > far);
+      in[j] = l[j] > edge || (l[j] == edge && e0 + i + 32 * j <= edge_at);
+      if (by_m) in[j] = in[j] && !(R.distance(l[j]) > far);
       any |= in[j];
       W[j] = 0;
     }
@@ -1053,9 +1036,12 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
     double w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) W[j] = weight(sm, l[j], R.dmax, R.s, &w[j]);
+    if (by_m) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (!in[j] || w[j] < mpd) W[j] = 0;
+      for (int j = 0; j < 4; ++j) in[j] = in[j] && w[j] >= mpd;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) W[j] = in[j] ? W[j] : 0ull;
   };
   unsigned long long m = 0, W[4];
 #pragma unroll 1
