@@ -158,79 +158,172 @@ __device__ __forceinline__ bool append_bounds(const AppendParams& p, int b, int*
   return *a >= 0 && *e >= *a && (int64_t)*e <= p.n_rows;
 }
 
-// Where one appended row goes: its staging row, and page and slot of its position; src < 0: nowhere.
-struct AppendTo {
-  int src, phys, slot;
+// A run: the appended rows of one sequence that go to one page.
+struct AppendRun {
+  int cnt;       // rows (0: nothing to write)
+  int row0;      // first packed row
+  int slot0;     // its slot in the page
+  int phys;
 };
 
-// The sequence of row i is searched by a warp (sequences with bad bounds hold no rows).
-__device__ __forceinline__ AppendTo append_to(const AppendParams& p, int64_t i, int lane, bool report) {
-  AppendTo t = {-1, 0, 0};
-  int b = -1;
-  for (int b0 = 0; b0 < p.B && b < 0; b0 += 32) {
-    int a = 0, e = 0;
-    const int x = b0 + lane;
-    const bool in = x < p.B && append_bounds(p, x, &a, &e) && a <= i && i < e;
-    const uint32_t here = __ballot_sync(0xffffffffu, in);
-    if (here) b = b0 + __ffs((int)here) - 1;
+// The id-th run of the call, by a whole warp.  Sequence b's rows take the places pos - 1 .. of its
+// cache, so its runs are the pages that these places touch; sequences with bad bounds have none.
+__device__ __forceinline__ AppendRun append_run(const AppendParams& p, int id, int lane, bool report) {
+  AppendRun r = {0, 0, 0, 0};
+  int before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int a = 0, e = 0, first = 0, runs = 0;
+    if (b < p.B && append_bounds(p, b, &a, &e) && e > a) {
+      first = p.pos[b];
+      // (a position below 1 is one run, which reports it)
+      runs = first >= 1 ? (int)(((int64_t)((first - 1) & 15) + (e - a) + 15) >> 4) : 1;
+    }
+    int inc = runs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const uint32_t here = __ballot_sync(0xffffffffu, id >= before + inc - runs && id < before + inc);
+    if (here) {
+      const int src = __ffs((int)here) - 1;
+      a = __shfl_sync(0xffffffffu, a, src);
+      e = __shfl_sync(0xffffffffu, e, src);
+      first = __shfl_sync(0xffffffffu, first, src);
+      const int k = id - before - __shfl_sync(0xffffffffu, inc - runs, src);
+      const int64_t page = (int64_t)((first - 1) >> 4) + k;
+      if (first < 1 || page >= p.max_pages) {
+        if (report && lane == 0) atomicOr(p.err, ODA_DEVERR_POS_RANGE);
+        return r;
+      }
+      const int off = (first - 1) & 15;                  // places before the first row in its page
+      const int lo = max(0, 16 * k - off), hi = (int)min((int64_t)(e - a), (int64_t)16 * (k + 1) - off);
+      r.cnt = hi - lo;
+      r.row0 = a + lo;
+      r.slot0 = (off + lo) & 15;
+      r.phys = p.page_table[(size_t)(b0 + src) * p.max_pages + page];
+      return r;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
   }
-  if (b < 0) return t;
-  const int first = p.pos[b];
-  const int64_t at = (int64_t)first - 1 + (i - p.cu[b]);        // 0-based place in the cache
-  if (first < 1 || at >= (int64_t)p.max_pages * kPageTok) {
-    if (report && lane == 0) atomicOr(p.err, ODA_DEVERR_POS_RANGE);
-    return t;
-  }
-  const int64_t src = p.rows ? p.rows[i] : i;
-  if (src < 0 || src >= p.n_stage) {
-    if (report && lane == 0) atomicOr(p.err, ODA_DEVERR_ROW_RANGE);
-    return t;
-  }
-  t.phys = p.page_table[(size_t)b * p.max_pages + at / kPageTok];
-  t.slot = (int)(at % kPageTok);
-  t.src = (int)src;
-  return t;
+  return r;
 }
 
-constexpr int kAppendRows = 16;
-
-// One CTA writes kAppendRows consecutive rows of one layer (blockIdx.y).
+// One CTA writes a run of one layer (blockIdx.y): rows of 256 bytes per head that are neighbours in the
+// page, so bf16 pages take whole lines, and an fp8 page's transposed V takes its tokens' bytes together.
 template <int F>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
-  __shared__ AppendTo to[kAppendRows];
+  __shared__ AppendRun run;
+  __shared__ int src[kPageTok];          // staging rows (< 0: none)
   const int l = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t i0 = (int64_t)blockIdx.x * kAppendRows;
-  for (int j = warp; j < kAppendRows; j += 8) {
-    AppendTo t = {-1, 0, 0};
-    if (i0 + j < p.n_rows) t = append_to(p, i0 + j, lane, l == 0);
-    if (t.src >= 0 && (t.phys < 0 || (int64_t)t.phys >= p.n_pages[l])) {
+  if (warp == 0) {
+    AppendRun r = append_run(p, blockIdx.x, lane, l == 0);
+    if (r.cnt > 0 && (r.phys < 0 || (int64_t)r.phys >= p.n_pages[l])) {
       if (lane == 0) atomicOr(p.err, ODA_DEVERR_PAGE_RANGE);
-      t.src = -1;
+      r.cnt = 0;
     }
-    if (lane == 0) to[j] = t;
+    if (lane == 0) run = r;
+    if (lane < r.cnt) {
+      const int64_t x = p.rows ? p.rows[r.row0 + lane] : r.row0 + lane;
+      const bool ok = x >= 0 && x < p.n_stage;
+      if (!ok && l == 0) atomicOr(p.err, ODA_DEVERR_ROW_RANGE);
+      src[lane] = ok ? (int)x : -1;
+    }
   }
   __syncthreads();
-  const int words = p.Hkv * 16;   // 16-byte words per row of K or V
+  const AppendRun r = run;
+  if (r.cnt == 0) return;
+  const int words = p.Hkv * 16;          // 16-byte words per row of K or V
   if constexpr (F == 0) {
-    for (int x = threadIdx.x; x < kAppendRows * 2 * words; x += blockDim.x) {
-      const int j = x / (2 * words), y = x - j * 2 * words;
-      const int which = y >= words, w = y - which * words;
-      const AppendTo t = to[j];
-      if (t.src < 0) continue;
-      const uint4 val = (which ? p.vs : p.ks)[((size_t)l * p.n_stage + t.src) * words + w];
+    // consecutive threads take a head's consecutive rows: the destination is contiguous
+    const int per = r.cnt * 16, all = 2 * p.Hkv * per;
+#pragma unroll 4
+    for (int x = threadIdx.x; x < all; x += 256) {
+      const int head = x / per, y = x - head * per;      // K heads, then V heads
+      const int which = head >= p.Hkv, h = head - which * p.Hkv, j = y >> 4, c = y & 15;
+      const int from = src[j];
+      if (from < 0) continue;
+      const uint4 val = __ldcs((which ? p.vs : p.ks) + ((size_t)l * p.n_stage + from) * words + h * 16 + c);
       uint4* pool = reinterpret_cast<uint4*>(which ? p.v[l] : p.k[l]);
-      pool[(((size_t)t.phys * p.Hkv + (w >> 4)) * kPageTok + t.slot) * 16 + (w & 15)] = val;
+      pool[(((size_t)r.phys * p.Hkv + h) * kPageTok + r.slot0 + j) * 16 + c] = val;
     }
   } else {
-    for (int x = warp; x < kAppendRows * 2 * p.Hkv; x += 8) {
-      const int j = x / (2 * p.Hkv), y = x - j * 2 * p.Hkv;
+    for (int y = warp; y < 2 * p.Hkv; y += 8) {
       const int which = y >= p.Hkv, h = y - which * p.Hkv;
-      const AppendTo t = to[j];
-      if (t.src < 0) continue;
-      const uint2 wv = reinterpret_cast<const uint2*>(which ? p.vs : p.ks)[(((size_t)l * p.n_stage + t.src) * words + h * 16) * 2 + lane];
-      float sc;
-      const uint32_t codes = quantize_row_e4m3(wv.x, wv.y, lane, &sc);
-      store_row_e4m3(static_cast<uint8_t*>(p.k[l]) + ((size_t)t.phys * p.Hkv + h) * kF8Block, which, t.slot, codes, sc, lane);
+      const uint2* rows = reinterpret_cast<const uint2*>(which ? p.vs : p.ks) + ((size_t)l * p.n_stage * words + h * 16) * 2;
+      uint8_t* blk = static_cast<uint8_t*>(p.k[l]) + ((size_t)r.phys * p.Hkv + h) * kF8Block;
+      // K: this lane has dims 4 lane .. + 3.  V: dims lane, 32 + lane, 64 + lane, 96 + lane, so that each of its
+      // stores takes 16 whole sectors of the transposed rows
+      uint32_t v[16];                    // V: this lane's 4 dims x 16 slots, one byte each
+      uint32_t have = 0;                 // slots filled
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0;
+#pragma unroll 1
+      for (int j0 = 0; j0 < r.cnt; j0 += 4) {
+        uint2 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int from = j0 + j < r.cnt ? src[j0 + j] : -1;
+          if (from < 0) continue;
+          const uint2* row = rows + (size_t)from * words * 2;
+          if (which == 0) {
+            w[j] = __ldcs(row + lane);
+          } else {
+            const unsigned short* x = reinterpret_cast<const unsigned short*>(row) + lane;
+            w[j].x = (uint32_t)__ldcs(x) | (uint32_t)__ldcs(x + 32) << 16;
+            w[j].y = (uint32_t)__ldcs(x + 64) | (uint32_t)__ldcs(x + 96) << 16;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j0 + j >= r.cnt || src[j0 + j] < 0) continue;
+          const int slot = r.slot0 + j0 + j;
+          float sc;
+          const uint32_t codes = quantize_row_e4m3(w[j].x, w[j].y, lane, &sc);
+          if (which == 0) {
+            store_row_e4m3(blk, 0, slot, codes, sc, lane);
+          } else {
+            const int sl = v8_slot(slot);
+            have |= 1u << sl;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if ((sl >> 2) == q) v[4 * d + q] |= ((codes >> (8 * d)) & 0xffu) << (8 * (sl & 3));
+            if (lane == 0) *reinterpret_cast<float*>(blk + kF8SV + 4 * slot) = sc;
+          }
+        }
+      }
+      if (which == 0) continue;
+      if (have == 0xffffu) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          *reinterpret_cast<uint4*>(blk + kF8V + 16 * (32 * d + lane)) = make_uint4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
+      } else {
+        // part of a page: words, pairs or single bytes, as they are filled
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t m = (have >> (4 * q)) & 0xfu;
+          if (!m) continue;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            uint8_t* to = blk + kF8V + 16 * (32 * d + lane) + 4 * q;
+            const uint32_t x = v[4 * d + q];
+            if (m == 0xfu) {
+              *reinterpret_cast<uint32_t*>(to) = x;
+              continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t two = (m >> (2 * i)) & 3u, y2 = x >> (16 * i);
+              if (two == 3u) *reinterpret_cast<uint16_t*>(to + 2 * i) = (uint16_t)y2;
+              else if (two == 1u) to[2 * i] = (uint8_t)y2;
+              else if (two == 2u) to[2 * i + 1] = (uint8_t)(y2 >> 8);
+            }
+          }
+        }
+      }
     }
   }
 }
@@ -395,7 +488,8 @@ oda_status launch_append(oda_ctx* ctx, const KvPool* layers, int32_t n_layers, c
   ctx->prev_attention = false;
   oda_status st = ODA_OK;
   if (n_rows > 0) {
-    const dim3 grid((unsigned)((n_rows + kAppendRows - 1) / kAppendRows), n_layers);
+    // runs: a sequence of n rows touches at most n / 16 + 2 pages
+    const dim3 grid((unsigned)(n_rows / kPageTok + 2 * std::min<int64_t>(n_rows, cf.batch)), n_layers);
     if (F == 0)
       append_kernel<0><<<grid, 256, 0, stream>>>(p);
     else

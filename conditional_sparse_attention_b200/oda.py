@@ -7,6 +7,7 @@ the context was created on; shapes follow include/oda.h.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence
 
 import torch
@@ -301,16 +302,29 @@ def oda_glue_gdn(ctx, st: OdaState, layer: int, c, v, alpha, beta, taps, flag, o
 
 # ------------------------------------------------- prompts, drafted trees, append, sampling
 def _want(name, t, dtypes, shape=None):
-    """A CUDA tensor of one of the element types and the given contiguous shape (None: any length)."""
+    """A CUDA tensor of one of the element types and, where given, of that contiguous shape."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and \
+            (shape is None or (t.shape == shape and t.is_contiguous())):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if shape is not None:
-        if t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape)):
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+@functools.lru_cache(maxsize=None)
+def _array_type(cls, n):
+    return cls * n
+
+
+def _array(cls, layers):
+    """The host array of layer descriptors that the library takes."""
+    arr = _array_type(cls, len(layers))()
+    arr[:] = layers
+    return arr
 
 
 _BF16 = (torch.bfloat16, torch.int16)
@@ -329,7 +343,7 @@ def _prompt_rows(name, t, heads):
 
 def _attend_prompt(fn, ctx, cu_rows, q, k, v, out, stream):
     Hq, Hkv = ctx.cfg.n_q_heads, ctx.cfg.n_kv_heads
-    _want("cu_rows", cu_rows, _I32, (None,))
+    _want("cu_rows", cu_rows, _I32, (cu_rows.numel(),))
     qs, ks, vs = _prompt_rows("q", q, Hq), _prompt_rows("k", k, Hkv), _prompt_rows("v", v, Hkv)
     n = int(q.shape[0])
     if k.shape[0] != n or v.shape[0] != n:
@@ -375,15 +389,15 @@ def oda_attend_full_tree(ctx, layer: OdaKVLayer, page_table, pos, flag, cu_rows,
 def _append(fn, cls, ctx, layers, page_table, pos, cu_rows, rows, k_stage, v_stage, h_stage, h_prev, pos_next,
             stream):
     c = ctx.cfg
-    arr = (cls * len(layers))(*layers)
+    arr = _array(cls, layers)
     _want("page_table", page_table, _I32, (c.batch, c.max_pages))
     _want("pos", pos, _I32, (c.batch,))
     _want("cu_rows", cu_rows, _I32, (c.batch + 1,))
-    _want("k_stage", k_stage, _BF16, (len(layers), None, c.n_kv_heads, 128))
-    n_stage = int(k_stage.shape[1])
+    n_stage = k_stage.shape[1] if k_stage.dim() == 4 else -1
+    _want("k_stage", k_stage, _BF16, (len(layers), n_stage, c.n_kv_heads, 128))
     _want("v_stage", v_stage, _BF16, (len(layers), n_stage, c.n_kv_heads, 128))
     if rows is not None:
-        _want("rows", rows, _I32, (None,))
+        _want("rows", rows, _I32, (rows.numel(),))
     if h_stage is not None:
         _want("h_stage", h_stage, _F32, (n_stage, c.head_in_dim))
     if h_prev is not None:
@@ -417,10 +431,13 @@ def oda_sample(ctx, logits, u, token, temperature=None, top_k=None, top_p=None, 
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits: expected [n, vocab] with contiguous rows")
     n, vocab = int(logits.shape[0]), int(logits.shape[1])
-    for name, t, dt in (("u", u, _F32), ("token", token, _I32), ("temperature", temperature, _F32),
-                        ("top_k", top_k, _I32), ("top_p", top_p, _F32), ("min_p", min_p, _F32), ("prob", prob, _F32)):
-        if t is not None or name in ("u", "token"):
-            _want(name, t, dt, (n,))
+    shape = (n,)
+    _want("u", u, _F32, shape)
+    _want("token", token, _I32, shape)
+    for name, t, dt in (("temperature", temperature, _F32), ("top_k", top_k, _I32), ("top_p", top_p, _F32),
+                        ("min_p", min_p, _F32), ("prob", prob, _F32)):
+        if t is not None:
+            _want(name, t, dt, shape)
     stride = logits.stride(0) if n > 1 else max(vocab, logits.stride(0))
     check(_lib.load().oda_sample(ctx.handle, n, vocab, stride, _p(logits), _p(temperature), _p(top_k), _p(top_p),
                                  _p(min_p), _p(u), _p(token), _p(prob), _s(stream)))

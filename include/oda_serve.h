@@ -17,7 +17,8 @@
  * Packed rows: the rows of sequence i are cu_rows[i] .. cu_rows[i+1] - 1 of every packed tensor
  * (device int32 [n_seqs + 1], 0 <= cu_rows[i] <= cu_rows[i+1] <= n_rows; a sequence may be empty).
  * Output rows outside all sequences are left as they were.  A sequence whose bounds break this rule
- * counts as empty and sets ODA_DEVERR_ROW_RANGE.
+ * counts as empty and sets ODA_DEVERR_ROW_RANGE; where bounds overlap, what the rows in common and
+ * behind them give is undefined.
  */
 #ifndef ODA_SERVE_H
 #define ODA_SERVE_H
