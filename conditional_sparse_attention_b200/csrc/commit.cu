@@ -38,8 +38,8 @@ __device__ __forceinline__ uint32_t quantize_row_e4m3(uint32_t w01, uint32_t w23
   const float x0 = bf16_lo_to_f32(w01), x1 = bf16_hi_to_f32(w01);
   const float x2 = bf16_lo_to_f32(w23), x3 = bf16_hi_to_f32(w23);
   float amax = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3)));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  // (the bits of values >= 0 are in their order; a lane of NaN alone counts as 0)
+  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, amax == amax ? __float_as_uint(amax) : 0u));
   const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
   *scale = s;
   const uint32_t c01 = f32x2_to_e4m3x2(__fdiv_rn(x0, s), __fdiv_rn(x1, s));
@@ -210,7 +210,7 @@ __device__ __forceinline__ AppendRun append_run(const AppendParams& p, int id, i
   return r;
 }
 
-// One CTA writes a run of one layer (blockIdx.y): rows of 256 bytes per head that are neighbours in the
+// One CTA writes a run of one layer (blockIdx.y).  Rows of 256 bytes per head that are neighbours in the
 // page, so bf16 pages take whole lines, and an fp8 page's transposed V takes its tokens' bytes together.
 template <int F>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
@@ -284,13 +284,18 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
           if (which == 0) {
             store_row_e4m3(blk, 0, slot, codes, sc, lane);
           } else {
-            const int sl = v8_slot(slot);
+            const int sl = v8_slot(slot), at = 4 * (sl & 3);
             have |= 1u << sl;
+            // byte d of the codes to byte sl mod 4 of word sl / 4 of dim d
+            const uint32_t keep = 0x3210u & ~(0xfu << at);
+            auto put = [&](int q) {
 #pragma unroll
-            for (int d = 0; d < 4; ++d)
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                if ((sl >> 2) == q) v[4 * d + q] |= ((codes >> (8 * d)) & 0xffu) << (8 * (sl & 3));
+              for (int d = 0; d < 4; ++d) v[4 * d + q] = __byte_perm(v[4 * d + q], codes, keep | (uint32_t)(4 + d) << at);
+            };
+            if ((sl >> 2) == 0) put(0);
+            else if ((sl >> 2) == 1) put(1);
+            else if ((sl >> 2) == 2) put(2);
+            else put(3);
             if (lane == 0) *reinterpret_cast<float*>(blk + kF8SV + 4 * slot) = sc;
           }
         }
@@ -305,21 +310,22 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint32_t m = (have >> (4 * q)) & 0xfu;
-          if (!m) continue;
+          uint8_t* to = blk + kF8V + 16 * lane + 4 * q;
+          if (m == 0xfu) {
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            uint8_t* to = blk + kF8V + 16 * (32 * d + lane) + 4 * q;
-            const uint32_t x = v[4 * d + q];
-            if (m == 0xfu) {
-              *reinterpret_cast<uint32_t*>(to) = x;
-              continue;
-            }
+            for (int d = 0; d < 4; ++d) *reinterpret_cast<uint32_t*>(to + 512 * d) = v[4 * d + q];
+            continue;
+          }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t two = (m >> (2 * i)) & 3u, y2 = x >> (16 * i);
-              if (two == 3u) *reinterpret_cast<uint16_t*>(to + 2 * i) = (uint16_t)y2;
-              else if (two == 1u) to[2 * i] = (uint8_t)y2;
-              else if (two == 2u) to[2 * i + 1] = (uint8_t)(y2 >> 8);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t two = (m >> (2 * i)) & 3u;
+            if (two == 3u) {
+#pragma unroll
+              for (int d = 0; d < 4; ++d) *reinterpret_cast<uint16_t*>(to + 512 * d + 2 * i) = (uint16_t)(v[4 * d + q] >> (16 * i));
+            } else if (two) {
+              const int odd = two == 2u, by = 16 * i + 8 * odd;
+#pragma unroll
+              for (int d = 0; d < 4; ++d) to[512 * d + 2 * i + odd] = (uint8_t)(v[4 * d + q] >> by);
             }
           }
         }
@@ -489,7 +495,8 @@ oda_status launch_append(oda_ctx* ctx, const KvPool* layers, int32_t n_layers, c
   oda_status st = ODA_OK;
   if (n_rows > 0) {
     // runs: a sequence of n rows touches at most n / 16 + 2 pages
-    const dim3 grid((unsigned)(n_rows / kPageTok + 2 * std::min<int64_t>(n_rows, cf.batch)), n_layers);
+    const int64_t runs = n_rows / kPageTok + 2 * std::min<int64_t>(n_rows, cf.batch);
+    const dim3 grid((unsigned)runs, n_layers);
     if (F == 0)
       append_kernel<0><<<grid, 256, 0, stream>>>(p);
     else
