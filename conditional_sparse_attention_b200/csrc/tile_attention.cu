@@ -687,11 +687,39 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       const int mine = jb.dual ? 0 : i;          // slot whose rows these are
       const int place = jb.tok0 + mine * p.nt + tok;
       const bool row_ok = tok < (mine ? jb.n1 : jb.n0);
+      // a warp without rows (small trees) only keeps the barriers' counts; its rows of P are whatever lies
+      // there, and its rows of O are never read (32 sequences, 16 nodes: 494 -> 456 us; prompts, which rarely
+      // have such warps, lose 3% to the registers it takes)
+      const bool idle = TREE && !__any_sync(0xffffffffu, row_ok);
       uint64_t anc = 0;
       if (TREE && row_ok && jb.first + jb.total > jb.node_tile) anc = ancestors(p.parent + jb.row0, place, p.err);
       const int cnt = slot_steps(jb, i);
+      // Rows behind the sequence in its last V tiles hold another one's values or old ones: their
+      // weights are 0, and 0 * NaN must not reach the sums.  Steps of 16 such rows are left out of the
+      // product; the rows of the last step are cleared here (by both slots: the same zeros).
+      auto clear_behind = [&](int t0, int x) {
+        const int valid = TREE ? (t0 >= jb.node_tile * kTile ? jb.len : jb.cached - t0) : jb.len - t0;
+        if (valid >= kTile || !(valid & 15)) return;
+        const uint32_t n = 2 * gs + order_v(jb, jb.dual ? 2 * x + i : x), st = n % kStages;
+        if (ok) ok = mbar_wait_bounded(&sm.kv_full[st], (n / kStages) & 1, kWaitNs);
+        const int rows = 16 - (valid & 15);
+        for (int z = half * kTile + r; z < rows * 16; z += 2 * kTile) {
+          const int row = valid + (z >> 4), ch = z & 15;
+          *reinterpret_cast<uint4*>(skv + st * kStageBytes + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      };
       float m = -INFINITY, l = 0.f;
       for (int x = 0; x < cnt; ++x) {
+        if (idle) {
+          if (ok) ok = mbar_wait_bounded(&sm.s_full[i], ns & 1, kWaitNs);
+          ++ns;
+          clear_behind(kv_tile(jb, jb.dual ? 2 * x + i : x) * kTile, x);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_ready[i][half]);
+          continue;
+        }
         // ---- which of this thread's columns the row sees
         const int t0 = kv_tile(jb, jb.dual ? 2 * x + i : x) * kTile, c0 = t0 + half * 64;
         uint32_t mw0, mw1;
@@ -757,23 +785,7 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             }
           }
         }
-        // Rows behind the sequence in its last V tiles hold another one's values or old ones: their
-        // weights are 0, and 0 * NaN must not reach the sums.  Steps of 16 such rows are left out of the
-        // product; the rows of the last step are cleared here (by both slots: the same zeros).
-        {
-          const int valid = TREE ? (t0 >= jb.node_tile * kTile ? jb.len : jb.cached - t0) : jb.len - t0;
-          if (valid < kTile && (valid & 15)) {
-            const uint32_t n = 2 * gs + order_v(jb, jb.dual ? 2 * x + i : x), st = n % kStages;
-            if (ok) ok = mbar_wait_bounded(&sm.kv_full[st], (n / kStages) & 1, kWaitNs);
-            const int rows = 16 - (valid & 15);
-            for (int z = half * kTile + r; z < rows * 16; z += 2 * kTile) {
-              const int row = valid + (z >> 4), ch = z & 15;
-              *reinterpret_cast<uint4*>(skv + st * kStageBytes + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-          }
-        }
+        clear_behind(t0, x);
         // ---- weights
         const float mc = m == -INFINITY ? 0.f : m * p.c;
         const uint64_t c2 = f32x2(p.c, p.c), mc2 = f32x2(-mc, -mc);
@@ -795,11 +807,13 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         if (ok) ok = mbar_wait_bounded(&sm.o_full[i], no & 1, kWaitNs);
         ++no;
         tc_fence_after();
-        if (half) sm.pair[i][r] = l;
-        pair_sync(meet);
-        if (!half) sm.pair[i][r] += l;
-        pair_sync(meet);
-        l = sm.pair[i][r];
+        if (!idle) {
+          if (half) sm.pair[i][r] = l;
+          pair_sync(meet);
+          if (!half) sm.pair[i][r] += l;
+          pair_sync(meet);
+          l = sm.pair[i][r];
+        }
       }
       float a0 = 1.f, a1 = 0.f;                  // factors of O0 and O1
       if (jb.dual) {
@@ -824,7 +838,7 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         m = nm;
         l = l * a0 + sm.pair[1][r] * a1;
       }
-      if (cnt > 0) {
+      if (cnt > 0 && !idle) {
         if (jb.direct) {
           const float inv = l > 0.f ? __fdividef(1.f, l) : (l == 0.f ? 0.f : l);
           a0 *= inv;
