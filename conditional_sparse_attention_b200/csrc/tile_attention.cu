@@ -897,15 +897,13 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   }
 }
 
-// Joins the partial results of the units that several CTAs shared: one warp per (node, query head).
-__global__ void __launch_bounds__(256) tree_join_kernel(const TileParams p, int grid) {
+// Joins the partial results of the units that several CTAs shared: a warp per (node, query head), blockIdx =
+// (node, group of 4 heads).
+__global__ void __launch_bounds__(128) tree_join_kernel(const TileParams p, uint32_t grid) {
   grid_dependency_wait();
-  const int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int64_t row = id / p.Hq;
-  const int head = (int)(id - row * p.Hq);
-  if (row >= p.n_rows) return;
+  const int row = blockIdx.x, lane = threadIdx.x & 31;
   int b = -1;                            // the sequence of this row, if it has tiles
+#pragma unroll 1
   for (int b0 = 0; b0 < p.n_seqs && b < 0; b0 += 32) {
     const int x = b0 + lane;
     const uint32_t here = __ballot_sync(0xffffffffu, x < p.n_seqs && p.cu[x] <= row && row < p.cu[x + 1] &&
@@ -914,42 +912,55 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TileParams p, int 
   }
   if (b < 0) return;
   const uint32_t before = p.plan[b], W = p.plan[p.n_seqs];
+  const int first = p.cu[b], len = p.cu[b + 1] - first, node = row - first, cached = p.pos[b] - 1;
   const uint32_t share = (W + grid - 1) / grid;
-  const int len = p.cu[b + 1] - p.cu[b], node = (int)(row - p.cu[b]);
-  const uint32_t tiles = (uint32_t)((p.pos[b] - 1 + kTile - 1) / kTile + 1);
-  const uint32_t M = (uint32_t)((len + 2 * p.nt - 1) / (2 * p.nt));
-  const uint32_t h = (uint32_t)(head / p.g), hh = (uint32_t)(head % p.g);
-  const uint32_t us = before + (h * M + (uint32_t)(node / (2 * p.nt))) * tiles, ue = us + tiles;
-  const uint32_t c0 = us / share, c1 = (ue - 1) / share;
-  if (c0 == c1) return;                                  // one CTA had it all and wrote it
-  const int in = node % (2 * p.nt);
-  const int r = (in / p.nt) * 128 + (in % p.nt) * p.g + (int)hh;
-  float m = -INFINITY;
-  for (uint32_t c = c0 + lane; c <= c1; c += 32) {
-    const size_t at = (size_t)(us > c * share ? 2 * c + 1 : 2 * c) * 256 + r;
-    m = fmaxf(m, p.part_ml[2 * at]);
-  }
+  const uint32_t tiles = (uint32_t)((cached + kTile - 1) / kTile + 1);
+  const uint32_t M = (uint32_t)((len + 2 * p.nt - 1) / (2 * p.nt)), unit = (uint32_t)(node / (2 * p.nt));
+  const int in = node % (2 * p.nt), r0 = (in / p.nt) * 128 + (in % p.nt) * p.g;
+  {
+    const int head = blockIdx.y * 4 + (threadIdx.x >> 5);
+    if (head >= p.Hq) return;
+    const uint32_t h = (uint32_t)(head / p.g), us = before + (h * M + unit) * tiles, ue = us + tiles;
+    const uint32_t c0 = us / share, c1 = (ue - 1) / share;
+    if (c0 == c1) return;                                // one CTA had it all and wrote it
+    const int r = r0 + head - (int)h * p.g;
+    // partial of CTA c: its first unit's, or its last one's; a lane has the statistics of each 32nd
+    auto part = [&](uint32_t c) { return (size_t)(us > c * share ? 2 * c + 1 : 2 * c) * 256 + r; };
+    float m = -INFINITY;
+    float2 ml = make_float2(-INFINITY, 0.f);
+#pragma unroll 1
+    for (uint32_t c = c0 + lane; c <= c1; c += 32) {
+      ml = reinterpret_cast<const float2*>(p.part_ml)[part(c)];
+      m = fmaxf(m, ml.x);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (uint32_t c = c0; c <= c1; ++c) {
-    const size_t at = (size_t)(us > c * share ? 2 * c + 1 : 2 * c) * 256 + r;
-    const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[at];
-    const float4 o = reinterpret_cast<const float4*>(p.part_o)[at * 32 + lane];
-    const float w = ml.x == m ? 1.f : exp2_approx((ml.x - m) * p.c);
-    l += w * ml.y;
-    acc.x += w * o.x;
-    acc.y += w * o.y;
-    acc.z += w * o.z;
-    acc.w += w * o.w;
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (uint32_t c = c0; c <= c1; c += 32) {
+      if (c1 - c0 >= 32) ml = c + lane <= c1 ? reinterpret_cast<const float2*>(p.part_ml)[part(c + lane)] : make_float2(-INFINITY, 0.f);
+      const float w = ml.x == m ? 1.f : exp2_approx((ml.x - m) * p.c);
+      l += w * ml.y;
+      const int n = (int)min(32u, c1 - c + 1);
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        const float4 o = reinterpret_cast<const float4*>(p.part_o)[part(c + j) * 32 + lane];
+        acc.x += wj * o.x;
+        acc.y += wj * o.y;
+        acc.z += wj * o.z;
+        acc.w += wj * o.w;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = __fdividef(1.f, l);
+    uint2 w;
+    w.x = cvt_bf16x2(acc.x * inv, acc.y * inv);
+    w.y = cvt_bf16x2(acc.z * inv, acc.w * inv);
+    reinterpret_cast<uint2*>(p.out)[((size_t)row * p.Hq + head) * 32 + lane] = w;
   }
-  const float inv = __fdividef(1.f, l);
-  uint2 w;
-  w.x = cvt_bf16x2(acc.x * inv, acc.y * inv);
-  w.y = cvt_bf16x2(acc.z * inv, acc.w * inv);
-  reinterpret_cast<uint2*>(p.out)[((size_t)row * p.Hq + head) * 32 + lane] = w;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1110,15 +1121,15 @@ oda_status launch_tree(oda_ctx* ctx, const oda_kv_layer* layer, const int32_t* p
   st = check_cuda(cudaGetLastError(), "tree attention launch");
   if (st != ODA_OK) return st;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)((n_rows * cf.n_q_heads + 7) / 8));
-  lc.blockDim = dim3(256);
+  lc.gridDim = dim3((unsigned)n_rows, (unsigned)((cf.n_q_heads + 3) / 4));
+  lc.blockDim = dim3(128);
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  return check_cuda(cudaLaunchKernelEx(&lc, tree_join_kernel, p, grid), "tree join launch");
+  return check_cuda(cudaLaunchKernelEx(&lc, tree_join_kernel, p, (uint32_t)grid), "tree join launch");
 }
 
 }  // namespace oda
