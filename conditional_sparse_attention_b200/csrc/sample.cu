@@ -80,6 +80,7 @@ struct Shared {
   Exchange wx[kWarps];
   Exchange found;
   uint32_t n_list;
+  uint32_t around[2];                    // values around the aim, and nearer than the window's far side
   unsigned long long list_mass;
 };
 
@@ -296,8 +297,7 @@ struct Row {                             // a CTA's view of its row
   int C, rank, tid, lane, warp;
   int turn;                              // exchanges so far
   int per;                               // values of a warp's contiguous part
-  float lmax;
-  float inv_t;
+  float half_max, inv_half;              // max / 2 and 2 / T
   double s, dmax;                        // 64 log2(e) / T, the maximum
   int32_t* err;
 
@@ -331,7 +331,8 @@ struct Row {                             // a CTA's view of its row
   __device__ unsigned long long sum_a(int t) { return warp_sum(lane < C ? remote(lane, t).a : 0ull); }
   __device__ uint32_t sum_c(int t) { return __reduce_add_sync(0xffffffffu, lane < C ? remote(lane, t).c : 0u); }
 
-  __device__ float distance(float l) const { return (lmax - l) * inv_t; }
+  // (max - l) / T; by halves, whose difference cannot overflow
+  __device__ float distance(float l) const { return fmaf(l, -0.5f, half_max) * inv_half; }
 
   // Four values 32 apart (-inf behind e).  Weights are made four abreast, since one alone is a chain of a
   // dozen fp64 operations.
@@ -358,7 +359,7 @@ struct Row {                             // a CTA's view of its row
     if (lane == 0) sm.wbeyond[warp] = beyond;
   }
 
-  __device__ int bin0(float l) const { return min(kBins - 1, (int)((lmax - l) * inv_t * 32.f)); }
+  __device__ int bin0(float l) const { return min(kBins - 1, (int)(distance(l) * 32.f)); }
 
   __device__ void add(int b, float l, bool mass) {
     atomicAdd(&cnt[b], 1u);
@@ -793,6 +794,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   cluster_arrive();                      // waited for before the first exchange
   if (tid < 64) sm.pow64[tid] = exp2((double)tid / 64.0);
   sm.coarse[tid] = 0;                    // kCoarse = kT
+  if (tid < 2) sm.around[tid] = 0;
 
   // ---- the row into shared memory.  Places are counted from the 16-byte boundary at or below
   // the row's first value, so all inner loads are 16 bytes wide.
@@ -831,7 +833,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   best = __reduce_max_sync(0xffffffffu, lane < kWarps ? sm.w32[lane] : 0u);
   const int per = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
   Row R = {sm, x, cnt, cnt + kBins, cnt + 2 * kBins, reinterpret_cast<unsigned long long*>(cnt + 3 * kBins),
-           e0, n, C, rank, tid, lane, warp, 0, per, 0.f, 1.f, 0.0, 0.0, p.err};
+           e0, n, C, rank, tid, lane, warp, 0, per, 0.f, 2.f, 0.0, 0.0, p.err};
   cluster_wait();                        // every CTA's barriers are there
   int t = R.exchange({0, 0, best, 0});
   best = __reduce_max_sync(0xffffffffu, lane < C ? R.remote(lane, t).c : 0u);
@@ -861,15 +863,16 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
     }
     return;
   }
-  R.lmax = of_key(best);
-  if (R.lmax == INFINITY) {              // only +inf counts, with equal weights
+  float lmax = of_key(best);
+  if (lmax == INFINITY) {              // only +inf counts, with equal weights
     __syncthreads();
     for (int i = tid; i < n; i += kT) x[i] = x[i] == INFINITY ? 0.f : -INFINITY;
-    R.lmax = 0.f;
+    lmax = 0.f;
     __syncthreads();
   }
-  R.inv_t = 1.f / T;
-  R.dmax = (double)R.lmax;
+  R.half_max = 0.5f * lmax;
+  R.inv_half = 2.f / T;
+  R.dmax = (double)lmax;
   R.s = 92.332482616893656769 / (double)T;              // 64 log2(e) / T
   const bool by_k = kk > 0 && kk < p.vocab, by_p = tp < 1.f, by_m = mp > 0.f;
   Cut cut = {0, 0x7fffffff};
@@ -878,7 +881,6 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
     unsigned long long mass = 0;
     const bool by_mass = !by_k;
     R.distances();
-    if (tid < 2) sm.w32[tid] = 0;
     cluster.sync();
     // ---- how far that is, to a few values, and a distance on both sides of it.  A bin a thread.
     float d1, d2;
@@ -906,13 +908,13 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
       const float mid = warp_sum(lane < kWarps ? __uint_as_float(sm.wx[lane].c) : 0.f);           // in bins
       // the values in the three bins around it, and half a window's width; the values nearer than its far end
       const uint32_t three = __reduce_add_sync(0xffffffffu, fabsf((float)tid + 0.5f - mid) < 1.5f ? c : 0u);
-      if (lane == 0 && three) atomicAdd(&sm.w32[0], three);
+      if (lane == 0 && three) atomicAdd(&sm.around[0], three);
       __syncthreads();
-      const float half = fminf(kCoarseBins, (float)(kWant / 2) * 3.f / (float)max(1u, sm.w32[0]));
+      const float half = fminf(kCoarseBins, (float)(kWant / 2) * 3.f / (float)max(1u, sm.around[0]));
       const uint32_t below = __reduce_add_sync(0xffffffffu, (float)tid < mid + half ? c : 0u);
-      if (lane == 0 && below) atomicAdd(&sm.w32[1], below);
+      if (lane == 0 && below) atomicAdd(&sm.around[1], below);
       __syncthreads();
-      d1 = sm.w32[1] <= (uint32_t)kList ? 0.f : fmaxf(0.f, mid - half) / kCoarseBins;
+      d1 = sm.around[1] <= (uint32_t)kList ? 0.f : fmaxf(0.f, mid - half) / kCoarseBins;
       d2 = (mid + half) / kCoarseBins;
       if (p.vocab <= kList) d1 = 0.f, d2 = INFINITY;
     }

@@ -171,3 +171,13 @@ def test_frequencies_follow_the_distribution(ctx):
     t, _ = _run(ctx, x, u)
     for i in range(6):
         assert abs((t == i).sum() - n * p[i]) < 6 * np.sqrt(n * p[i] * (1 - p[i]))
+
+
+@pytest.mark.parametrize("vocab", [50, 5000, 60000])
+@pytest.mark.parametrize("kw", [dict(top_p=0.8), dict(top_k=20), dict(min_p=0.01), dict(top_k=30, top_p=0.7)])
+def test_logits_whose_differences_leave_fp32(ctx, vocab, kw):
+    """Logits of both signs near fp32's largest, under a temperature of their size."""
+    r = np.random.RandomState(vocab)
+    logits = ((r.rand(6, vocab) * 2 - 1) * 3.3e38).astype(np.float32)
+    logits[1] = np.where(r.rand(vocab) < 0.5, np.float32(3.4e38), np.float32(-3.4e38))
+    _check(ctx, logits, r.rand(6), temperature=1e38, **kw)
