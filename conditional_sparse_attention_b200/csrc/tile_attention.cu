@@ -760,12 +760,16 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           top0 = max3(top0, __uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]));
           top1 = max3(top1, __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
         }
-        const float top = fmaxf(top0, top1);
-        const bool grow = top * p.c > m * p.c + kGrow;   // also the first finite value (m = -inf)
+        const float top = max3(top0, top1, top1);
+        // also the first finite value (m = -inf), and a NaN that the row sees, which stays the reference
+        const bool grow = row_ok && !(top * p.c <= m * p.c + kGrow);
         if (pair_or(meet, grow)) {
           if (half) sm.pair[i][r] = top;
           pair_sync(meet);
-          if (!half) sm.pair[i][r] = max3(m, top, sm.pair[i][r]);
+          if (!half) {
+            const float nm = max3(m, top, sm.pair[i][r]);
+            sm.pair[i][r] = nm < INFINITY ? nm : NAN;    // +inf has no finite weight beside it
+          }
           pair_sync(meet);
           const float nm = sm.pair[i][r];
           const float al = m == nm ? 1.f : exp2_approx((m - nm) * p.c);
@@ -840,7 +844,7 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       }
       if (cnt > 0 && !idle) {
         if (jb.direct) {
-          const float inv = l > 0.f ? __fdividef(1.f, l) : (l == 0.f ? 0.f : l);
+          const float inv = m > -INFINITY ? __fdividef(1.f, l) : NAN;   // (every score -inf: no weights)
           a0 *= inv;
           a1 *= inv;
         }
@@ -955,7 +959,7 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TileParams p, uint
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = __fdividef(1.f, l);
+    const float inv = m > -INFINITY ? __fdividef(1.f, l) : NAN;
     uint2 w;
     w.x = cvt_bf16x2(acc.x * inv, acc.y * inv);
     w.y = cvt_bf16x2(acc.z * inv, acc.w * inv);

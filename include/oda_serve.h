@@ -44,7 +44,9 @@ extern "C" {
  * may be columns of one projection output); out: bf16 [n_rows][Hq][128].  q, k, v and out 16-byte
  * aligned.  Products of bf16 operands with fp32 sums; softmax statistics fp32; the weights are
  * rounded to bf16 before the product with V, and the output once at the end.  A NaN or infinity in
- * one sequence's rows never reaches another sequence; within its own sequence it may reach any row. */
+ * one sequence's rows never reaches another sequence.  Within its own, one of k reaches the rows that see
+ * it, as the formula says (NaN, but for a score of -inf beside finite ones, whose weight is 0); one of v
+ * makes every row that sees it NaN and may make others NaN. */
 oda_status oda_attend_full_prompt(oda_ctx* ctx, int32_t n_seqs, int64_t n_rows,
                                   const int32_t* cu_rows, const void* q, const void* k,
                                   const void* v, int64_t q_stride, int64_t kv_stride, void* out,
@@ -65,8 +67,8 @@ oda_status oda_attend_local_prompt(oda_ctx* ctx, int32_t n_seqs, int64_t n_rows,
  * out: bf16 [n_rows][Hq][128]; all 16-byte aligned; 1 <= n_rows <= batch*ODA_MAX_TREE (0 nodes:
  * cu_rows all equal).  Rows of skipped sequences are left as they were.  A page-table entry outside
  * the pool sets ODA_DEVERR_PAGE_RANGE, a position outside the table's capacity ODA_DEVERR_POS_RANGE
- * (the sequence is skipped); the outputs of a sequence with a bad page are undefined.  Arithmetic as
- * the prompt calls; the cached range is split over the SMs and joined in a fixed order, so equal
+ * (the sequence is skipped); the outputs of a sequence with a bad page are undefined.  Arithmetic and
+ * what NaN and infinities reach as in the prompt calls; the cached range is split over the SMs and joined in a fixed order, so equal
  * calls give equal bits. */
 oda_status oda_attend_full_tree(oda_ctx* ctx, const oda_kv_layer* layer, const int32_t* page_table,
                                 const int32_t* pos, const int32_t* flag, int64_t n_rows,
@@ -112,8 +114,11 @@ oda_status oda_append_fp8(oda_ctx* ctx, const oda_kv8_layer* layers, int32_t n_l
  * T <= 0 or NaN: the lowest index of the largest logit, prob 1.  NaN and -inf logits are masked (never
  * chosen); where +inf logits are present only they count, with equal weights; a row with nothing
  * left gives token -1 and prob 0.  u is clamped to [0, 1), NaN counts as 0.  Weights are computed in
- * 64 bits and summed as 64-bit whole numbers (multiples of 2^-43 of the largest weight or finer; smaller
- * weights are masked), so the result does not depend on the order of any sum. */
+ * 64 bits and summed as whole multiples of 2^-43 of the largest weight (smaller weights count as 0), so the
+ * draw does not depend on the order of any sum.  Top-p without top-k over
+ * more than 1024 values places its end with fp32 sums of the weights below e^-3 of the largest, in an order
+ * that depends only on the row's length and its place modulo 16 bytes: equal calls give equal bits, and
+ * the end may lie a value off where a running mass meets top_p within some 1e-7 of it. */
 oda_status oda_sample(oda_ctx* ctx, int32_t n_rows, int32_t vocab, int64_t row_stride,
                       const float* logits, const float* temperature, const int32_t* top_k,
                       const float* top_p, const float* min_p, const float* u, int32_t* token,

@@ -216,3 +216,38 @@ def test_bad_bounds_are_reported_and_skipped():
                 keep = 30 if cu == [0, 40, 30, 100] else e - a   # rows 30..39 belong to two sequences there
                 check_attention(got[:keep], o[:keep], m[:keep])
     ctx.close()
+
+
+@pytest.mark.parametrize("j", [3, 70, 135, 263])
+@pytest.mark.parametrize("local", [False, True])
+def test_rows_that_see_a_nan_key_are_nan(j, local):
+    """A NaN key: every row that sees it is NaN, the others are as they were.  An infinite one: NaN where
+    its score is +inf; as if it were not there where the score is -inf; NaN where every score is."""
+    n, hq, hkv, window = 400, 4, 2, 100
+    gen = torch.Generator(device="cuda").manual_seed(j)
+    q, k, v = normal(gen, n, hq, 128), normal(gen, n, hkv, 128), normal(gen, n, hkv, 128)
+    q[:, 0::2, 9], q[:, 1::2, 9] = 1.0, -1.0
+    ctx = _ctx(hq, hkv, 2, window)
+    t = np.arange(n)
+    sees = (t >= j) & ((t < j + window) | (not local))
+    for bad in (float("nan"), float("inf")):
+        k1 = k.clone()
+        k1[j, :, 9] = bad
+        out = torch.zeros(n, hq, 128, dtype=torch.bfloat16, device="cuda")
+        _run(ctx, local, cumulative([n]), q, k1, v, out)
+        torch.cuda.synchronize()
+        got, ok = f64(out), (t[None, :] <= t[:, None])
+        if local:
+            ok &= (t[None, :] < 2) | (t[None, :] > t[:, None] - window)
+        ok[:, j] = False
+        for h in range(hq):
+            odd = h % 2 == 1 and bad > 0             # score -inf
+            o, a = serve._rows(f64(q[:, h]), f64(k[:, h // 2]), f64(v[:, h // 2]), ok)
+            rows = np.ones(n, bool) if odd else ~sees
+            check_attention(got[rows, h], o[rows], a[rows], (h, bad))
+            assert odd or np.isnan(got[sees, h]).all()
+    k1 = k.clone()
+    k1[:, :, 9] = float("inf")                       # every score of an odd head is -inf, of an even one +inf
+    _run(ctx, local, cumulative([n]), q, k1, v, out)
+    assert torch.isnan(out).all()
+    ctx.close()

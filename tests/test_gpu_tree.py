@@ -185,3 +185,49 @@ def test_bad_data_is_reported():
     e, out = call(cu=(4, 0, 9))
     assert e == 0x8 and torch.all(out[0:0] == 7.0)
     ctx.close()
+
+
+@pytest.mark.parametrize("place", [6, 1000, 3000])
+def test_nodes_that_see_a_nan_key_are_nan(place):
+    """A NaN key in the cache reaches every node of its sequence, one of a node itself and its descendants;
+    other sequences none.  Infinite keys: as in the formula."""
+    from conditional_sparse_attention_b200 import oda
+    hq, hkv, lens, nodes = 4, 2, [3100, 50], [24, 5]
+    gen = torch.Generator(device="cuda").manual_seed(place)
+    r = np.random.RandomState(place)
+    kp, vp, pt, caches = make_pages(lens, hkv, gen)
+    N = sum(nodes)
+    q, kn, vn = normal(gen, N, hq, 128), normal(gen, N, hkv, 128), normal(gen, N, hkv, 128)
+    parents = [_parents(r, n, "random") for n in nodes]
+    par = torch.tensor([x for p in parents for x in p], dtype=torch.int32, device="cuda")
+    ctx = oda.oda_create(oda.make_config(2, hq, hkv, pt.shape[1], 512))
+    pos = torch.tensor([n + 1 for n in lens], dtype=torch.int32, device="cuda")
+
+    def run(kp, kn):
+        out = torch.zeros(N, hq, 128, dtype=torch.bfloat16, device="cuda")
+        oda.oda_attend_full_tree(ctx, oda.kv_layer(kp, vp), pt, pos, None, cumulative(nodes), par, q, kn, vn, out)
+        torch.cuda.synchronize()
+        return f64(out)
+    want = [serve.tree(f64(q[s]), *map(f64, caches[b]), f64(kn[s]), f64(vn[s]), parents[b])
+            for b, s in enumerate((slice(0, 24), slice(24, 29)))]
+    bad = kp.clone()
+    bad[pt[0, place // 16].item(), :, place % 16, 7] = float("nan")
+    got = run(bad, kn)
+    assert np.isnan(got[:24]).all()
+    check_attention(got[24:], *want[1])
+    bad = kn.clone()
+    bad[6, :, 50] = float("nan")
+    got = run(kp, bad)
+    sees = serve.lineage(parents[0])[:, 6]
+    assert np.isnan(got[:24][sees]).all()
+    check_attention(got[:24][~sees], want[0][0][~sees], want[0][1][~sees])
+    check_attention(got[24:], *want[1])
+    # every score of sequence 0 is -inf (cache and nodes), and a row of +inf
+    q[:, :, 9] = -1.0
+    kb, nb = kp.clone(), kn.clone()
+    kb[pt[0, :194].long(), :, :, 9] = float("inf")
+    nb[:24, :, 9] = float("inf")
+    assert np.isnan(run(kb, nb)[:24]).all()
+    q[:, :, 9] = 1.0
+    assert np.isnan(run(kb, nb)[:24]).all()
+    ctx.close()
