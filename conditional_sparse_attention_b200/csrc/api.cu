@@ -338,8 +338,19 @@ oda_status oda_commit_fp8(oda_ctx* ctx, const oda_kv8_layer* layers, int32_t n_l
                             stream);
 }
 
-static oda_status append_pools(oda_ctx* ctx, const void* layers, int32_t n_layers) {
-  if (!ctx) return set_error(ODA_ERR_INVALID_ARG, "append: ctx is NULL");
+// The context, and the current device its own: a launch elsewhere would run on another GPU.
+static oda_status serve_ctx(const oda_ctx* ctx, const char* who) {
+  if (!ctx) return set_error(ODA_ERR_INVALID_ARG, "%s: ctx is NULL", who);
+  int device = -1;
+  const oda_status st = check_cuda(cudaGetDevice(&device), "cudaGetDevice");
+  if (st == ODA_OK && device != ctx->device)
+    return set_error(ODA_ERR_INVALID_ARG, "%s: the context is of device %d, the current one is %d", who, ctx->device, device);
+  return st;
+}
+
+static oda_status append_pools(const oda_ctx* ctx, const void* layers, int32_t n_layers) {
+  const oda_status st = serve_ctx(ctx, "append");
+  if (st != ODA_OK) return st;
   if (!layers || n_layers < 1 || n_layers > ODA_MAX_LAYERS)
     return set_error(ODA_ERR_INVALID_ARG, "append: n_layers must be 1..%d", ODA_MAX_LAYERS);
   return ODA_OK;
@@ -375,7 +386,8 @@ oda_status oda_attend_full_prompt(oda_ctx* ctx, int32_t n_seqs, int64_t n_rows,
                                   const int32_t* cu_rows, const void* q, const void* k,
                                   const void* v, int64_t q_stride, int64_t kv_stride, void* out,
                                   cudaStream_t stream) {
-  if (!ctx) return set_error(ODA_ERR_INVALID_ARG, "attend_full_prompt: ctx is NULL");
+  const oda_status st = serve_ctx(ctx, "attend_full_prompt");
+  if (st != ODA_OK) return st;
   return oda::launch_prompt(ctx, n_seqs, n_rows, cu_rows, q, k, v, q_stride, kv_stride, out, 0, stream);
 }
 
@@ -383,7 +395,8 @@ oda_status oda_attend_local_prompt(oda_ctx* ctx, int32_t n_seqs, int64_t n_rows,
                                    const int32_t* cu_rows, const void* q, const void* k,
                                    const void* v, int64_t q_stride, int64_t kv_stride, void* out,
                                    cudaStream_t stream) {
-  if (!ctx) return set_error(ODA_ERR_INVALID_ARG, "attend_local_prompt: ctx is NULL");
+  const oda_status st = serve_ctx(ctx, "attend_local_prompt");
+  if (st != ODA_OK) return st;
   return oda::launch_prompt(ctx, n_seqs, n_rows, cu_rows, q, k, v, q_stride, kv_stride, out, 1, stream);
 }
 
@@ -392,7 +405,8 @@ oda_status oda_attend_full_tree(oda_ctx* ctx, const oda_kv_layer* layer, const i
                                 const int32_t* cu_rows, const int32_t* parent, const void* q,
                                 const void* k_new, const void* v_new, void* out,
                                 cudaStream_t stream) {
-  if (!ctx) return set_error(ODA_ERR_INVALID_ARG, "attend_full_tree: ctx is NULL");
+  const oda_status st = serve_ctx(ctx, "attend_full_tree");
+  if (st != ODA_OK) return st;
   return oda::launch_tree(ctx, layer, page_table, pos, flag, n_rows, cu_rows, parent, q, k_new, v_new, out, stream);
 }
 
@@ -400,7 +414,8 @@ oda_status oda_sample(oda_ctx* ctx, int32_t n_rows, int32_t vocab, int64_t row_s
                       const float* logits, const float* temperature, const int32_t* top_k,
                       const float* top_p, const float* min_p, const float* u, int32_t* token,
                       float* prob, cudaStream_t stream) {
-  if (!ctx) return set_error(ODA_ERR_INVALID_ARG, "sample: ctx is NULL");
+  const oda_status st = serve_ctx(ctx, "sample");
+  if (st != ODA_OK) return st;
   return oda::launch_sample(ctx, n_rows, vocab, row_stride, logits, temperature, top_k, top_p, min_p, u,
                             token, prob, stream);
 }

@@ -338,7 +338,7 @@ def _prompt_rows(name, t, heads):
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128 or t.stride(2) != 1 or \
             (heads > 1 and t.stride(1) != 128):
         raise ValueError(f"{name}: expected rows [n, {heads}, 128] with contiguous heads")
-    return t.stride(0) if t.shape[0] > 1 else max(heads * 128, t.stride(0))
+    return t.stride(0) if t.shape[0] > 1 else heads * 128
 
 
 def _attend_prompt(fn, ctx, cu_rows, q, k, v, out, stream):
@@ -438,7 +438,7 @@ def oda_sample(ctx, logits, u, token, temperature=None, top_k=None, top_p=None, 
                         ("min_p", min_p, _F32), ("prob", prob, _F32)):
         if t is not None:
             _want(name, t, dt, shape)
-    stride = logits.stride(0) if n > 1 else max(vocab, logits.stride(0))
+    stride = logits.stride(0) if n > 1 else vocab
     check(_lib.load().oda_sample(ctx.handle, n, vocab, stride, _p(logits), _p(temperature), _p(top_k), _p(top_p),
                                  _p(min_p), _p(u), _p(token), _p(prob), _s(stream)))
 

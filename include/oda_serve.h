@@ -11,8 +11,9 @@
  *
  * Same conventions as oda.h: device pointers unless stated otherwise, asynchronous on `stream`, no
  * allocation, graph capturable, calls on one context ordered on one stream, argument errors returned
- * before anything is launched, data-dependent violations reported in the context's error word.  Heads,
- * sinks, window, page table width and batch come from the context's configuration.
+ * before anything is launched (a context of another device than the current one among them), data-
+ * dependent violations reported in the context's error word.  Heads, sinks, window, page table width and
+ * batch come from the context's configuration.
  *
  * Packed rows: the rows of sequence i are cu_rows[i] .. cu_rows[i+1] - 1 of every packed tensor
  * (device int32 [n_seqs + 1], 0 <= cu_rows[i] <= cu_rows[i+1] <= n_rows; a sequence may be empty).

@@ -229,3 +229,22 @@ def test_empty_calls():
     assert oda.oda_get_error(ctx) == 0
     assert torch.all(out == 3.0) and torch.all(kp == 3.0) and nxt.tolist() == [5, 9]
     ctx.close()
+
+
+def test_one_row_of_any_stride():
+    """A single row has no stride: a view whose row stride fits no rule is taken."""
+    from conditional_sparse_attention_b200 import oda
+    ctx = oda.oda_create(oda.make_config(1, 2, 1, 3, 512))
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    buf = normal(gen, 4 * 1001)
+    q = buf.as_strided((1, 2, 128), (1001, 128, 1))
+    k = buf.as_strided((1, 1, 128), (3, 128, 1), 1024)
+    v = buf.as_strided((1, 1, 128), (1001, 128, 1), 2048)
+    out = torch.zeros(1, 2, 128, dtype=torch.bfloat16, device="cuda")
+    oda.oda_attend_full_prompt(ctx, cumulative([1]), q, k, v, out)
+    logits = torch.randn(90, generator=gen, device="cuda").as_strided((1, 50), (3, 1), 7)
+    token = torch.zeros(1, **I32)
+    oda.oda_sample(ctx, logits, torch.zeros(1, device="cuda"), token, temperature=torch.zeros(1, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(out, v.expand(1, 2, 128)) and token.item() == logits.argmax().item()
+    ctx.close()
