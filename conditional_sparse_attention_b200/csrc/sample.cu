@@ -91,9 +91,11 @@ constexpr double kC2 = kL * kL / 2, kC3 = kL * kL * kL / 6, kC4 = kL * kL * kL *
 // Weight e^((l - max)/T) of logit l, and as a whole multiple of 2^-kFrac; s = 64 log2(e) / T.  No branch, so
 // that the weights of a loop run abreast; -inf gives 0.
 __device__ __forceinline__ unsigned long long weight(const Shared& sm, float l, double max, double s, double* w) {
-  const double y0 = ((double)l - max) * s;              // <= 0, -inf, or NaN (0 * inf: the maximum itself)
-  const bool in = !(y0 <= -64.0 * (kFrac + 1)) && l > -INFINITY;   // below half a step the weight is 0
-  const double y = in && y0 == y0 ? y0 : 0.0;
+  const double y0 = ((double)l - max) * s;              // <= 0 (s is finite for every T > 0); -inf or NaN for l = -inf
+  // |y0| < 64 (kFrac + 1) = 2816 by its high word: below half a step the weight is 0
+  static_assert(kFrac == 43, "the word below is -2816's");
+  const bool in = (uint32_t)__double2hiint(y0) < 0xc0a60000u && l > -INFINITY;
+  const double y = in ? y0 : 0.0;
   const double t = y + 6755399441055744.0;              // 1.5 * 2^52: rounds to a whole number, in the low bits
   const double r = y - (t - 6755399441055744.0);
   const int k = (int)__double_as_longlong(t);
@@ -1019,72 +1021,112 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   // (a distance that min-p cannot reach; 2^-20 covers the rounding of the distances)
   const float far = by_m ? -logf(fminf(mp, 1.f)) * (1.f + 0x1p-20f) + 0x1p-20f : INFINITY;
   const int a = min(n, warp * per), e = min(n, a + per);
-  // the masses of 4 values 32 apart from i on (0 where dropped)
   const bool cuts = cut.key > kMasked;  // else every unmasked value stays
   const float edge = cuts ? of_key(cut.key) : -INFINITY;
   const int edge_at = cuts ? cut.at : -1;
-  auto kept4 = [&](int i, unsigned long long* W) {
-    float l[4];
-    R.load4(i, e, l);
-    bool in[4], any = false;
+  // 4 values 32 apart from i on that the cut (and, but for roundings, min-p) keeps, else -inf
+  auto kept4 = [&](int i, int to, float* l) {
+    R.load4(i, to, l);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      in[j] = l[j] > edge || (l[j] == edge && e0 + i + 32 * j <= edge_at);
-      if (by_m) in[j] = in[j] && !(R.distance(l[j]) > far);
-      any |= in[j];
-      W[j] = 0;
+      bool in = l[j] > edge || (l[j] == edge && e0 + i + 32 * j <= edge_at);
+      if (by_m) in = in && !(R.distance(l[j]) > far);
+      if (!in) l[j] = -INFINITY;
     }
-    if (!__any_sync(0xffffffffu, any)) return;
+  };
+  auto masses4 = [&](const float* l, unsigned long long* W) {
     double w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) W[j] = weight(sm, l[j], R.dmax, R.s, &w[j]);
     if (by_m) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) in[j] = in[j] && w[j] >= mpd;
+      for (int j = 0; j < 4; ++j) W[j] = w[j] >= mpd ? W[j] : 0ull;
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) W[j] = in[j] ? W[j] : 0ull;
   };
   unsigned long long m = 0, W[4];
+  float l[4];
+  if (!cuts && !by_m) {
 #pragma unroll 1
-  for (int i = a + lane; i - lane < e; i += 128) {
-    kept4(i, W);
+    for (int i = a + lane; i - lane < e; i += 128) {
+      kept4(i, e, l);
+      masses4(l, W);
+      m += (W[0] + W[1]) + (W[2] + W[3]);
+    }
+  } else {
+    // few are kept: closed up in 256 places of the warp's own, and weighed 128 at a time
+    __syncthreads();                     // (CTA 0's list lay there)
+    float* buf = reinterpret_cast<float*>(cnt) + 256 * warp;
+    uint32_t fill = 0;
+#pragma unroll 1
+    for (int i = a + lane; true; i += 128) {
+      const bool more = i - lane < e;
+      if (more) {
+        kept4(i, e, l);
+        if (!__any_sync(0xffffffffu, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) > -INFINITY)) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t in = __ballot_sync(0xffffffffu, l[j] > -INFINITY);
+          if (l[j] > -INFINITY) buf[fill + __popc(in & ((1u << lane) - 1u))] = l[j];
+          fill += __popc(in);
+        }
+        if (fill < 128) continue;
+      }
+      __syncwarp();
+      const uint32_t from = fill > 128 ? fill - 128 : 0;     // (behind the last, fill < 128)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) l[j] = from + 32 * j + lane < fill ? buf[from + 32 * j + lane] : -INFINITY;
+      masses4(l, W);
+      m += (W[0] + W[1]) + (W[2] + W[3]);
+      fill = from;
+      __syncwarp();
+      if (!more) break;
+    }
+  }
+  m = warp_sum(m);
+  __syncthreads();
+  if (lane == 0) sm.w64[warp] = m;
+  __syncthreads();
+  const unsigned long long here = warp_sum(lane < kWarps ? sm.w64[lane] : 0ull);
+  t = R.exchange({here, 0, 0, 0});
+  const unsigned long long theirs = lane < C ? R.remote(lane, t).a : 0ull;
+  unsigned long long before = warp_sum(lane < rank ? theirs : 0ull);
+  const unsigned long long total = warp_sum(theirs);
+  const unsigned long long want = min((unsigned long long)((double)u * (double)total), total - 1);
+  if (want < before || want >= before + here) return;    // the draw is another CTA's
+  // ---- the element: the warp's part that holds it, which all warps share out, then the share
+  auto part = [&]() {                    // index of the warp's mass that holds it; before: all in front
+    const unsigned long long mass = lane < kWarps ? sm.w64[lane] : 0ull, upto = before + warp_scan(mass, lane);
+    const int at = __ffs((int)__ballot_sync(0xffffffffu, want < upto)) - 1;
+    before = __shfl_sync(0xffffffffu, upto - mass, at);
+    return at;
+  };
+  const int a1 = min(n, part() * per), e1w = min(n, a1 + per), per2 = (per / kWarps + 31) / 32 * 32;
+  const int a2 = min(e1w, a1 + warp * per2), e2 = min(e1w, a2 + per2);
+  m = 0;
+#pragma unroll 1
+  for (int i = a2 + lane; i - lane < e2; i += 128) {
+    kept4(i, e2, l);
+    masses4(l, W);
     m += (W[0] + W[1]) + (W[2] + W[3]);
   }
   m = warp_sum(m);
   __syncthreads();
   if (lane == 0) sm.w64[warp] = m;
   __syncthreads();
-  unsigned long long before = 0, here = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sm.w64[w];
-    here += sm.w64[w];
-  }
-  t = R.exchange({here, 0, 0, 0});
-  const unsigned long long theirs = lane < C ? R.remote(lane, t).a : 0ull;
-  before += warp_sum(lane < rank ? theirs : 0ull);
-  const unsigned long long total = warp_sum(theirs);
-  const unsigned long long want = min((unsigned long long)((double)u * (double)total), total - 1);
-  if (before <= want && want < before + m) {             // one warp of the cluster
-    unsigned long long run = before;
+  if (part() != warp) return;
 #pragma unroll 1
-    for (int i = a + lane; i - lane < e; i += 128) {
-      kept4(i, W);
-      const unsigned long long all = warp_sum((W[0] + W[1]) + (W[2] + W[3]));
-      if (want >= run + all) {
-        run += all;
-        continue;
+  for (int i = a2 + lane; i - lane < e2; i += 128) {
+    kept4(i, e2, l);
+    masses4(l, W);
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      const unsigned long long upto = before + warp_scan(W[0], lane);
+      if (upto - W[0] <= want && want < upto) {
+        p.token[row] = e0 + i + 32 * j - mis;
+        if (p.prob) p.prob[row] = (float)((double)W[0] / (double)total);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const unsigned long long upto = run + warp_scan(W[j], lane);
-        if (upto - W[j] <= want && want < upto) {
-          p.token[row] = e0 + i + 32 * j - mis;
-          if (p.prob) p.prob[row] = (float)((double)W[j] / (double)total);
-        }
-        run = __shfl_sync(0xffffffffu, upto, 31);
-      }
-      break;
+      before = __shfl_sync(0xffffffffu, upto, 31);
+      W[0] = W[1], W[1] = W[2], W[2] = W[3];
     }
   }
 }
