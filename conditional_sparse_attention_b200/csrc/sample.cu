@@ -40,6 +40,7 @@ constexpr int kWarps = kT / 32;
 constexpr int kMaxC = 8;                 // CTAs of a cluster
 constexpr int kBins = 1024;
 constexpr int kList = 1024;
+constexpr int kShort = 192;              // listed values that are compared in pairs
 constexpr int kSeg = 5120;               // values of a CTA above which the cluster grows
 constexpr int kFrac = 43;                // weights are multiples of 2^-43
 constexpr int kCoarse = 512;              // bins of the histogram that aims
@@ -605,10 +606,65 @@ struct Row {                             // a CTA's view of its row
     return drop;
   }
 
+  // The same for a short list, a thread a value: every thread sums what lies above its own (a list of
+  // 2: 9600 -> 2700 clocks, one of 150: 8200 -> 7200).
+  __device__ void draw_short(int m, bool whole, int kk, float tp, float mp, unsigned long long mass, float u, int* token,
+                             float* prob) {
+    const uint32_t* key = cnt;
+    unsigned long long* W = reinterpret_cast<unsigned long long*>(cnt + 2 * kList);
+    const uint32_t own = tid < m ? key[tid] : 0u;
+    unsigned long long w = 0;
+    double x = 0.0;
+    if (tid < m) w = weight(sm, of_key(own), dmax, s, &x);
+    if (tid < (m + 3) / 4 * 4) W[tid] = w, cnt[tid] = own;   // (key 0: in front of nothing)
+    __syncthreads();
+    unsigned long long above = 0;        // mass and number of the values in front, largest first, ties by place
+    uint32_t number = 0;
+    if (32 * warp < m) {
+#pragma unroll 1
+      for (int j = 0; j < m; j += 4) {
+        const uint4 k4 = *reinterpret_cast<const uint4*>(key + j);
+        const ulonglong2 w01 = *reinterpret_cast<const ulonglong2*>(W + j), w23 = *reinterpret_cast<const ulonglong2*>(W + j + 2);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        const unsigned long long v[4] = {w01.x, w01.y, w23.x, w23.y};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bool front = k[q] >= (j + q < tid ? own : own + 1u);
+          above += front ? v[q] : 0ull;  // (no branch: all lanes differ)
+          number += front ? 1u : 0u;
+        }
+      }
+    }
+    bool keep = tid < m && (kk <= 0 || number < (uint32_t)kk);
+    auto sum = [&](unsigned long long v, unsigned long long* before) {
+      const unsigned long long run = warp_scan(v, lane);
+      __syncthreads();
+      if (lane == 31) sm.w64[warp] = run;
+      __syncthreads();
+      const unsigned long long each = lane < kWarps ? sm.w64[lane] : 0ull;
+      *before = run - v + warp_sum(lane < warp ? each : 0ull);
+      return warp_sum(each);
+    };
+    unsigned long long before;
+    if (tp < 1.f) {
+      if (whole || kk > 0) mass = sum(keep ? w : 0ull, &before);
+      const double want = tp > 0.f ? ceil((double)tp * (double)mass) : 1.0;
+      keep = keep && above < max(1ull, min((unsigned long long)want, mass));
+    }
+    if (mp > 0.f) keep = keep && x >= fmin((double)mp, 1.0);
+    const unsigned long long total = sum(keep ? w : 0ull, &before);
+    const unsigned long long want = min((unsigned long long)((double)u * (double)total), total - 1);
+    if (keep && before <= want && want < before + w) {
+      *token = (int)cnt[kList + tid];
+      *prob = (float)((double)w / (double)total);
+    }
+  }
+
   // CTA 0 draws from the m listed values, which hold every cut (`mass`: top-p's total without top-k; `whole`: they
   // are the row's all).
   __device__ void draw_list(int m, bool whole, int kk, float tp, float mp, unsigned long long mass, float u, int* token,
                             float* prob) {
+    if (m <= kShort) return draw_short(m, whole, kk, tp, mp, mass, u, token, prob);
     const bool by_p = tp < 1.f;
     const uint32_t* key = cnt;
     const uint32_t* place = cnt + kList;
