@@ -40,6 +40,7 @@ constexpr int kWarps = kT / 32;
 constexpr int kMaxC = 8;                 // CTAs of a cluster
 constexpr int kBins = 1024;
 constexpr int kList = 1024;
+constexpr int kBatch = 5;               // 16-byte loads of a thread in flight
 constexpr int kShort = 192;              // listed values that are compared in pairs
 constexpr int kSeg = 5120;               // values of a CTA above which the cluster grows
 constexpr int kFrac = 43;                // weights are multiples of 2^-43
@@ -80,6 +81,8 @@ struct Shared {
   uint32_t wk[kWarps];
   Exchange wx[kWarps];
   Exchange found;
+  float temperature, top_p, min_p, u;    // the row's settings
+  int top_k;
   uint32_t n_list;
   uint32_t around[2];                    // values around the aim, and nearer than the window's far side
   unsigned long long list_mass;
@@ -850,6 +853,13 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
     fence_mbar_init();
   }
   cluster_arrive();                      // waited for before the first exchange
+  if (tid == kT - 1) {                   // (the settings on their way while the row comes)
+    sm.temperature = p.temperature ? p.temperature[row] : 1.f;
+    sm.top_k = p.top_k ? p.top_k[row] : 0;
+    sm.top_p = p.top_p ? p.top_p[row] : 1.f;
+    sm.min_p = p.min_p ? p.min_p[row] : 0.f;
+    sm.u = p.u[row];
+  }
   if (tid < 64) sm.pow64[tid] = exp2((double)tid / 64.0);
   sm.coarse[tid] = 0;                    // kCoarse = kT
   if (tid < 2) sm.around[tid] = 0;
@@ -867,22 +877,30 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
     return l;
   };
   const float* at0 = src - mis;
-#pragma unroll 5
-  for (int i = 4 * tid; i < n; i += 4 * kT) {
-    const int e = e0 + i;
-    float4 v;
-    if (e >= mis && e + 4 <= p.vocab + mis) {
-      v = __ldcs(reinterpret_cast<const float4*>(at0 + e));
-    } else {
-      float t[4];
-      for (int j = 0; j < 4; ++j) t[j] = (e + j >= mis && e + j < p.vocab + mis) ? at0[e + j] : -INFINITY;
-      v = make_float4(t[0], t[1], t[2], t[3]);
+  // kBatch loads of a thread in flight together, the two ends of the row apart
+#pragma unroll 1
+  for (int i0 = 4 * tid; i0 < n; i0 += kBatch * 4 * kT) {
+    float4 v[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int i = i0 + q * 4 * kT, e = e0 + i;
+      if (i < n && e >= mis && e + 4 <= p.vocab + mis) v[q] = __ldcs(reinterpret_cast<const float4*>(at0 + e));
     }
-    v.x = take(v.x);
-    v.y = take(v.y);
-    v.z = take(v.z);
-    v.w = take(v.w);
-    *reinterpret_cast<float4*>(x + i) = v;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int i = i0 + q * 4 * kT, e = e0 + i;
+      if (i >= n) break;
+      if (e < mis || e + 4 > p.vocab + mis) {
+        float t[4];
+        for (int j = 0; j < 4; ++j) t[j] = (e + j >= mis && e + j < p.vocab + mis) ? at0[e + j] : -INFINITY;
+        v[q] = make_float4(t[0], t[1], t[2], t[3]);
+      }
+      v[q].x = take(v[q].x);
+      v[q].y = take(v[q].y);
+      v[q].z = take(v[q].z);
+      v[q].w = take(v[q].w);
+      *reinterpret_cast<float4*>(x + i) = v[q];
+    }
   }
   // ---- the maximum
   best = __reduce_max_sync(0xffffffffu, best);
@@ -896,11 +914,9 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   int t = R.exchange({0, 0, best, 0});
   best = __reduce_max_sync(0xffffffffu, lane < C ? R.remote(lane, t).c : 0u);
   // ---- settings
-  const float T = p.temperature ? p.temperature[row] : 1.f;
-  const int kk = p.top_k ? p.top_k[row] : 0;
-  const float tp = p.top_p ? p.top_p[row] : 1.f;
-  const float mp = p.min_p ? p.min_p[row] : 0.f;
-  float u = p.u[row];
+  const float T = sm.temperature, tp = sm.top_p, mp = sm.min_p;
+  const int kk = sm.top_k;
+  float u = sm.u;
   u = u >= 0.f ? fminf(u, 1.f) : 0.f;
   const bool none = best == kMasked;
   if (none || !(T > 0.f)) {              // the same for the whole cluster
@@ -1104,8 +1120,10 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   if (!cuts && !by_m) {
 #pragma unroll 1
     for (int i = a + lane; i - lane < e; i += 128) {
-      kept4(i, e, l);
-      masses4(l, W);
+      double w;
+      R.load4(i, e, l);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) W[j] = weight(sm, l[j], R.dmax, R.s, &w);
       m += (W[0] + W[1]) + (W[2] + W[3]);
     }
   } else {
