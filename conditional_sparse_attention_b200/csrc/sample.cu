@@ -346,14 +346,20 @@ struct Row {                             // a CTA's view of its row
 #pragma unroll
     for (int j = 0; j < 4; ++j) l[j] = i + 32 * j < e ? x[i + 32 * j] : -INFINITY;
   }
+  // The same of four neighbours, for passes without an order (i a multiple of 4; x is filled up to one with -inf).
+  __device__ void load4v(int i, int e, float* l) const {
+    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (i < e) v = *reinterpret_cast<const float4*>(x + i);
+    l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
+  }
   // The CTA's values by distance, and the mass of those behind the last bin.
   __device__ void distances() {
     const int a = min(n, warp * per), e = min(n, a + per);
     float beyond = 0.f;
 #pragma unroll 1
-    for (int i = a + lane; i - lane < e; i += 128) {
+    for (int i = a + 4 * lane; i - 4 * lane < e; i += 128) {
       float l[4];
-      load4(i, e, l);
+      load4v(i, e, l);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float d = distance(l[j]), b = d * kCoarseBins;
@@ -496,10 +502,10 @@ struct Row {                             // a CTA's view of its row
     Exchange v = {};
     float f1 = 0.f, f2 = 0.f, f = 0.f;
 #pragma unroll 1
-    for (int i = a + lane; i - lane < e; i += 128) {
+    for (int i = a + 4 * lane; i - 4 * lane < e; i += 128) {
       float l[4], d[4];
       bool close = false;
-      load4(i, e, l);
+      load4v(i, e, l);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         d[j] = distance(l[j]);
@@ -1119,9 +1125,9 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   float l[4];
   if (!cuts && !by_m) {
 #pragma unroll 1
-    for (int i = a + lane; i - lane < e; i += 128) {
+    for (int i = a + 4 * lane; i - 4 * lane < e; i += 128) {
       double w;
-      R.load4(i, e, l);
+      R.load4v(i, e, l);
 #pragma unroll
       for (int j = 0; j < 4; ++j) W[j] = weight(sm, l[j], R.dmax, R.s, &w);
       m += (W[0] + W[1]) + (W[2] + W[3]);
