@@ -30,8 +30,8 @@ def _p(t) -> ctypes.c_void_p:
 
 
 def _s(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:                   # the current stream's handle, without a Stream object (3 us a call)
+        return _c(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return _c(stream)
     return _c(stream.cuda_stream)
@@ -333,25 +333,25 @@ _F32 = (torch.float32,)
 
 
 def _prompt_rows(name, t, heads):
-    """Row stride of packed rows [n, heads, 128] whose heads are contiguous inside a row."""
+    """Number and row stride of packed rows [n, heads, 128] whose heads are contiguous inside a row."""
     _want(name, t, _BF16)
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128 or t.stride(2) != 1 or \
-            (heads > 1 and t.stride(1) != 128):
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or sh[1] != heads or sh[2] != 128 or st[2] != 1 or (heads > 1 and st[1] != 128):
         raise ValueError(f"{name}: expected rows [n, {heads}, 128] with contiguous heads")
-    return t.stride(0) if t.shape[0] > 1 else heads * 128
+    return sh[0], (st[0] if sh[0] > 1 else heads * 128)
 
 
 def _attend_prompt(fn, ctx, cu_rows, q, k, v, out, stream):
     Hq, Hkv = ctx.cfg.n_q_heads, ctx.cfg.n_kv_heads
-    _want("cu_rows", cu_rows, _I32, (cu_rows.numel(),))
-    qs, ks, vs = _prompt_rows("q", q, Hq), _prompt_rows("k", k, Hkv), _prompt_rows("v", v, Hkv)
-    n = int(q.shape[0])
-    if k.shape[0] != n or v.shape[0] != n:
+    n_cu = cu_rows.numel()
+    _want("cu_rows", cu_rows, _I32, (n_cu,))
+    (n, qs), (nk, ks), (nv, vs) = _prompt_rows("q", q, Hq), _prompt_rows("k", k, Hkv), _prompt_rows("v", v, Hkv)
+    if nk != n or nv != n:
         raise ValueError("q, k and v must have the same number of rows")
     if ks != vs:
         raise ValueError("k and v must have the same row stride")
     _want("out", out, _BF16, (n, Hq, 128))
-    check(fn(ctx.handle, int(cu_rows.shape[0]) - 1, n, _p(cu_rows), _p(q), _p(k), _p(v), qs, ks, _p(out),
+    check(fn(ctx.handle, n_cu - 1, n, _p(cu_rows), _p(q), _p(k), _p(v), qs, ks, _p(out),
              _s(stream)))
 
 
