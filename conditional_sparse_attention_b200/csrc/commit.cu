@@ -212,6 +212,11 @@ __device__ __forceinline__ AppendRun append_run(const AppendParams& p, int id, i
 
 // One CTA writes a run of one layer (blockIdx.y).  Rows of 256 bytes per head that are neighbours in the
 // page, so bf16 pages take whole lines, and an fp8 page's transposed V takes its tokens' bytes together.
+// Bound, bf16: the copy (two prompts of 900..2100 into 28 layers, 871 MB: 150 us, 5.8 TB/s, 89% of the measured
+// copy).  fp8, few rows: instructions, some 220 a warp and row (the exact division by the scale, the bytes of
+// the transposed V) at half the issue rate; accepted paths of 32 sequences into 36 layers: 31 us, 27 MB.  A
+// warp a run, layer and head, without barriers, took 36 us where this takes 28 (L2 warm), several layers a CTA
+// were slower too.
 template <int F>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   __shared__ AppendRun run;

@@ -7,8 +7,9 @@
 //   2. for top-k and top-p a histogram over the distance d = (max - l) / T, in 512 bins of 1/32
 //   3. it tells closely how far the cut lies (a bin's weights differ by 3%).  Exact counts and masses within
 //      two distances around that (again with others where they miss it) leave a window of at most 1024
-//      values, which go to CTA 0 in index order; it finds the last one kept (16 thresholds a round, one a
-//      warp).  Where the window begins at the maximum CTA 0 drops by min-p and draws, and the others leave.
+//      values, which go to CTA 0 in index order; it finds the last one kept (by 8 bits of the values at a
+//      time, or in pairs).  Where the window begins at the maximum CTA 0 drops by min-p and draws, and the
+//      others leave.
 //   4. else the masses of the survivors, a prefix over warps and CTAs, and the element at u * mass
 //   5. where no window is found (many equal values, masked or extreme rows, top-p of a large top-k): a
 //      histogram over d in 1024 bins of 1/32, counts and masses, gives the bin of the cut, whose values
@@ -17,11 +18,15 @@
 //
 // Weights e^-d are computed in fp64 (table of 2^(j/64) and a Taylor polynomial of degree 4, relative
 // error below 5e-14) and held as whole multiples of 2^-43 of the largest weight: sums of whole numbers do not
-// depend on their order, so neither atomics nor the cluster's shape can change a token.  A row of
-// ODA_MAX_VOCAB = 2^18 weights sums to at most 2^61.
+// depend on their order, so neither atomics nor the cluster's shape can change a draw.  (Only step 3's
+// masses beyond d = 3 are fp32 sums, each in a fixed order.)  A row of ODA_MAX_VOCAB = 2^18 weights sums to
+// at most 2^61.
 //
-// Bound: HBM for the row, then the fp64 pipe (some 12 operations a weight at 64 lanes a clock and SM)
-// and, for few rows, the latency of the cluster's barriers.
+// Bound: latency.  A row of 152k values is 0.6 MB, 0.1 us of HBM, and its phases wait for one another: some
+// 4500 clocks for the row, 2000 for the maximum, 12000 for step 2, 7000 for a pass of step 3, 2500 to 9000 for
+// CTA 0's part, 13000 for step 4 (where every value survives, the fp64 pipe: some 11 operations a weight at 64
+// lanes a clock and SM).  Two CTAs an SM overlap theirs.  Measured at 151936 values, settings mixed, data not
+// in L2: one row 21 us, 32 rows 38 us, 256 rows 205 us (0.8 TB/s); greedy 256 rows 70 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>

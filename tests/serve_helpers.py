@@ -6,8 +6,8 @@ BF16_HALF = 2.0 ** -8      # half a step of bf16, relative
 # Error of one output element against fp64 (A = the softmax-weighted mean of |v|, o the exact output):
 #   weights rounded to bf16 before the product with V:            at most 2^-8 A
 #   fp32 scores: sums of 128 products, |q.k| / sqrt(128) off by at most 128 * 2^-24 * sum |q_i k_i| /
-#     sqrt(128) (about 1e-4 at the tests' values), once in the weights and once in their sum; exp2 and
-#     the fp32 sums below 1e-5; together below 2^-11 A
+#     sqrt(128) (about 1e-4 at the tests' values), once in the weights and once in their sum; exp2 (a
+#     quarter of them by a cubic, 7.5e-5) and the fp32 sums below 1e-4; together below 2^-11 = 4.9e-4 A
 #   the result rounded to bf16:                                   at most 2^-8 of what is rounded,
 #     2^-8 (|o| + the above)
 W_SLACK = BF16_HALF + 2.0 ** -11
