@@ -40,11 +40,24 @@ __device__ __forceinline__ uint32_t quantize_row_e4m3(uint32_t w01, uint32_t w23
   float amax = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3)));
   // (the bits of values >= 0 are in their order; a lane of NaN alone counts as 0)
   amax = __uint_as_float(__reduce_max_sync(0xffffffffu, amax == amax ? __float_as_uint(amax) : 0u));
-  const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+  float s = 1.0f, q0, q1, q2, q3;
+  if (amax >= 0x1p-80f && amax <= 0x1p100f) {
+    // The same roundings by a reciprocal (Markstein): r = RN(1 / b), q = RN(a r), RN(q + r (a - q b)) is RN(a / b)
+    // where a - q b is exact.  Here it is for every quotient of 2^-11 or more (s >= 2^-89, so its products with
+    // a quotient's last place reach down to 2^-145); a smaller one is a code of 0 however it is rounded.
+    auto quotient = [](float a, float by, float r) {
+      const float q = a * r;
+      return fmaf(r, fmaf(-q, by, a), q);
+    };
+    s = quotient(amax, 448.0f, 1.0f / 448.0f);
+    const float r = __frcp_rn(s);
+    q0 = quotient(x0, s, r), q1 = quotient(x1, s, r), q2 = quotient(x2, s, r), q3 = quotient(x3, s, r);
+  } else {
+    if (amax > 0.f) s = __fdiv_rn(amax, 448.0f);
+    q0 = __fdiv_rn(x0, s), q1 = __fdiv_rn(x1, s), q2 = __fdiv_rn(x2, s), q3 = __fdiv_rn(x3, s);
+  }
   *scale = s;
-  const uint32_t c01 = f32x2_to_e4m3x2(__fdiv_rn(x0, s), __fdiv_rn(x1, s));
-  const uint32_t c23 = f32x2_to_e4m3x2(__fdiv_rn(x2, s), __fdiv_rn(x3, s));
-  return c01 | (c23 << 16);
+  return f32x2_to_e4m3x2(q0, q1) | (f32x2_to_e4m3x2(q2, q3) << 16);
 }
 
 // Writes a quantised token row (K if which == 0, else V) into slot j of a block.

@@ -164,3 +164,36 @@ def test_bad_data_is_reported_and_not_written(fmt):
     e, t, _ = call([0, 2, 20], [1, 1], None, bad)
     assert e == 0x1 and t == both((1, 1))
     ctx.close()
+
+
+def test_fp8_rows_of_every_scale():
+    """Rows whose largest value is 2^-133 .. 2^127: codes and scales of IEEE divisions, bit for bit."""
+    from conditional_sparse_attention_b200 import oda
+    n = 261
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(1, n, 1, 128, generator=gen, device="cuda", dtype=torch.float64)
+    x = x / x.abs().amax(-1, keepdim=True) * torch.exp2(torch.arange(n, device="cuda", dtype=torch.float64).view(1, n, 1, 1) - 133)
+    x[:, :, :, ::3] *= torch.exp2(-torch.arange(43, device="cuda", dtype=torch.float64) / 3)     # down to codes of 0
+    ks, vs = x.to(torch.bfloat16), x.flip(1).to(torch.bfloat16)
+    mp = (n + 15) // 16
+    ctx = oda.oda_create(oda.make_config(1, 1, 1, mp, 512))
+    pool = torch.zeros(mp, 1, 4224, dtype=torch.uint8, device="cuda")
+    i32 = lambda y: torch.tensor(y, dtype=torch.int32, device="cuda")  # noqa: E731
+    oda.oda_append_fp8(ctx, [oda.kv8_layer(pool)], torch.arange(mp, **dict(dtype=torch.int32, device="cuda")).view(1, mp),
+                       i32([1]), i32([0, n]), None, ks, vs)
+    assert oda.oda_get_error(ctx) == 0
+    got = pool.cpu().numpy()
+    for which, rows in ((0, ks), (1, vs)):
+        f = rows[0, :, 0].float().cpu()
+        amax = f.abs().amax(-1)
+        s = torch.where(amax > 0, amax / torch.tensor(448.0), torch.tensor(1.0))
+        codes = (f / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+        for j in range(n):
+            blk, t = got[j // 16, 0], j % 16
+            assert blk[4096 + 64 * which + 4 * t:][:4].tobytes() == s[j].numpy().tobytes(), (which, j)
+            if which == 0:
+                c = np.concatenate([blk[128 * t + 16 * (k ^ (t & 7)):][:16] for k in range(8)])
+            else:
+                c = blk[2048:4096].reshape(128, 16)[:, 4 * ((t & 7) >> 1) + ((t >> 3) << 1) + (t & 1)]
+            assert np.array_equal(c, codes[j]), (which, j)
+    ctx.close()
