@@ -224,16 +224,17 @@ __device__ __forceinline__ AppendRun append_run(const AppendParams& p, int id, i
 }
 
 // One CTA writes a run of one layer (blockIdx.y).  Rows of 256 bytes per head that are neighbours in the
-// page, so bf16 pages take whole lines, and an fp8 page's transposed V takes its tokens' bytes together.
+// page, so bf16 pages take whole lines, and an fp8 page's transposed V is written whole.
 // Bound, bf16: the copy (two prompts of 900..2100 into 28 layers, 871 MB: 150 us, 5.8 TB/s, 89% of the measured
-// copy).  fp8, few rows: instructions, some 220 a warp and row (the exact division by the scale, the bytes of
-// the transposed V) at half the issue rate; accepted paths of 32 sequences into 36 layers: 31 us, 27 MB.  A
-// warp a run, layer and head, without barriers, took 36 us where this takes 28 (L2 warm), several layers a CTA
-// were slower too.
+// copy).  fp8, few rows: latency and instructions, a CTA's lookups and then some 150 instructions a warp and row;
+// accepted paths of 32 sequences into 36 layers, 27 MB: 27 us (22.7 with L2 warm; 28 with a V page's bytes written
+// one by one and IEEE divisions).  Slower: a warp a run, layer and head without barriers, several layers a
+// CTA, CTAs of 128 or 512 threads, 48 registers for a fifth CTA an SM.
 template <int F>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   __shared__ AppendRun run;
   __shared__ int src[kPageTok];          // staging rows (< 0: none)
+  __shared__ bool part;                  // some slots of the page are left as they are
   const int l = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     AppendRun r = append_run(p, blockIdx.x, lane, l == 0);
@@ -248,6 +249,10 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
       if (!ok && l == 0) atomicOr(p.err, ODA_DEVERR_ROW_RANGE);
       src[lane] = ok ? (int)x : -1;
     }
+    __syncwarp();
+    if (lane == 0) part = false;
+    __syncwarp();
+    if (r.cnt < kPageTok ? lane == 0 : lane < kPageTok && src[lane] < 0) part = true;
   }
   __syncthreads();
   const AppendRun r = run;
@@ -271,12 +276,16 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
       const int which = y >= p.Hkv, h = y - which * p.Hkv;
       const uint2* rows = reinterpret_cast<const uint2*>(which ? p.vs : p.ks) + ((size_t)l * p.n_stage * words + h * 16) * 2;
       uint8_t* blk = static_cast<uint8_t*>(p.k[l]) + ((size_t)r.phys * p.Hkv + h) * kF8Block;
-      // K: this lane has dims 4 lane .. + 3.  V: dims lane, 32 + lane, 64 + lane, 96 + lane, so that each of its
-      // stores takes 16 whole sectors of the transposed rows
-      uint32_t v[16];                    // V: this lane's 4 dims x 16 slots, one byte each
-      uint32_t have = 0;                 // slots filled
+      // K: this lane has dims 4 lane .. + 3.  V: dims lane, 32 + lane, 64 + lane, 96 + lane, each with its 16 slots,
+      // one byte each, in v: the transposed rows that it writes whole, 512 bytes a store.  Where the run fills
+      // only part of the page they are read first (no other warp of the call writes this page's V).
+      uint32_t v[16];
+      uint4* line = reinterpret_cast<uint4*>(blk + kF8V) + lane;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0;
+      for (int d = 0; d < 4; ++d) {
+        const uint4 old = which && part ? line[32 * d] : make_uint4(0, 0, 0, 0);
+        v[4 * d] = old.x, v[4 * d + 1] = old.y, v[4 * d + 2] = old.z, v[4 * d + 3] = old.w;
+      }
 #pragma unroll 1
       for (int j0 = 0; j0 < r.cnt; j0 += 4) {
         uint2 w[4];
@@ -303,7 +312,6 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
             store_row_e4m3(blk, 0, slot, codes, sc, lane);
           } else {
             const int sl = v8_slot(slot), at = 4 * (sl & 3);
-            have |= 1u << sl;
             // byte d of the codes to byte sl mod 4 of word sl / 4 of dim d
             const uint32_t keep = 0x3210u & ~(0xfu << at);
             auto put = [&](int q) {
@@ -319,35 +327,8 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
         }
       }
       if (which == 0) continue;
-      if (have == 0xffffu) {
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
-          *reinterpret_cast<uint4*>(blk + kF8V + 16 * (32 * d + lane)) = make_uint4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
-      } else {
-        // part of a page: words, pairs or single bytes, as they are filled
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t m = (have >> (4 * q)) & 0xfu;
-          uint8_t* to = blk + kF8V + 16 * lane + 4 * q;
-          if (m == 0xfu) {
-#pragma unroll
-            for (int d = 0; d < 4; ++d) *reinterpret_cast<uint32_t*>(to + 512 * d) = v[4 * d + q];
-            continue;
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t two = (m >> (2 * i)) & 3u;
-            if (two == 3u) {
-#pragma unroll
-              for (int d = 0; d < 4; ++d) *reinterpret_cast<uint16_t*>(to + 512 * d + 2 * i) = (uint16_t)(v[4 * d + q] >> (16 * i));
-            } else if (two) {
-              const int odd = two == 2u, by = 16 * i + 8 * odd;
-#pragma unroll
-              for (int d = 0; d < 4; ++d) to[512 * d + 2 * i + odd] = (uint8_t)(v[4 * d + q] >> by);
-            }
-          }
-        }
-      }
+      for (int d = 0; d < 4; ++d) line[32 * d] = make_uint4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
     }
   }
 }
