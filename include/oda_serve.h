@@ -95,7 +95,9 @@ oda_status oda_append(oda_ctx* ctx, const oda_kv_layer* layers, int32_t n_layers
                       const int32_t* cu_rows, const int32_t* rows, const void* k_stage,
                       const void* v_stage, const float* h_stage, float* h_prev, int32_t* pos_next,
                       cudaStream_t stream);
-/* The same into fp8 pages: every row is quantised as oda_commit_fp8 does. */
+/* The same into fp8 pages: every row is quantised as oda_commit_fp8 does.  A page that is filled in part is
+ * read and written back with its other bytes, so sequences must not share a page that they write to, and
+ * calls that run at once must not write to the same one. */
 oda_status oda_append_fp8(oda_ctx* ctx, const oda_kv8_layer* layers, int32_t n_layers,
                           const int32_t* page_table, const int32_t* pos, int64_t n_rows,
                           int64_t n_stage, const int32_t* cu_rows, const int32_t* rows,
