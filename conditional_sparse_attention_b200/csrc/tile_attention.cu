@@ -31,7 +31,7 @@
 //     895 TFLOP/s of the pairs in the set (the tiles at the window's two ends and the sinks' tile are partly
 //     masked: 18 tiles for 16).  One token: 7.4 us; 512 tokens, 16/8 heads: 14.5 us.
 //   trees: the cache's bytes while a KV head has few rows (32 sequences of 2000..32768, 16 nodes, 16/8 heads:
-//     426 us, 5.5 TB/s, 84%), then the products (4 of 131072, 64 nodes, 32/8 heads: 594 us, 3.6 TB/s and 835
+//     418 us, 5.6 TB/s, 86%), then the products (4 of 131072, 64 nodes, 32/8 heads: 586 us, 3.7 TB/s and 847
 //     TFLOP/s at once).  A chain of 5 over 4096 positions: 20 us, of which the join is 5.
 #include <algorithm>
 #include <cmath>
@@ -107,6 +107,13 @@ struct Smem {
   uint32_t pref[ODA_MAX_BATCH + 1];     // prompt: blocks of each sequence; tree: tiles before it
 };
 constexpr int kTileBytes = (2 + kStages) * kStageBytes;   // Q slots, then K and V stages
+// A V tile in shared memory, one half of 64 dims behind the other.  Prompts: halves of 128 positions.  Trees: a
+// page's 16 positions, both halves, one page behind the other, so that a page comes in one copy.  (K tiles, whose
+// 8-row groups have to lie evenly, are halves of 128 positions in both.)
+template <bool TREE>
+constexpr int kVHalf = TREE ? 2048 : kHalf;
+template <bool TREE>
+constexpr int kV16 = TREE ? 4096 : 2048;  // bytes from 16 positions to the next
 constexpr int kDynBytes = kTileBytes + sizeof(Smem);
 static_assert(kDynBytes <= 227 * 1024, "shared memory of a CTA");
 
@@ -526,20 +533,24 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         } else if (t == jb.node_tile) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&sm.kv_full[st], ODA_MAX_TREE * 256);
-            for (int h2 = 0; h2 < 2; ++h2)
-              tma_load_3d(dst + h2 * kHalf, w ? &mvn : &mkn, h2 * 64, jb.h, jb.row0, &sm.kv_full[st]);
+            if (w)
+              for (int i = 0; i < ODA_MAX_TREE / 16; ++i)
+                tma_load_4d(dst + i * kV16<TREE>, &mvn, 0, jb.row0 + 16 * i, 0, jb.h, &sm.kv_full[st]);
+            else
+              for (int h2 = 0; h2 < 2; ++h2) tma_load_3d(dst + h2 * kHalf, &mkn, h2 * 64, jb.h, jb.row0, &sm.kv_full[st]);
           }
         } else {
           const int pages = min(8, (jb.cached - t * kTile + 15) / 16);
           if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[st], (uint32_t)(pages * 4096));
           __syncwarp();
-          if (lane < 2 * pages) {
+          if (lane < 2 * pages && (w == 0 || hf == 0)) {
             int64_t row = ((int64_t)page * p.Hkv + jb.h) * 16;
             if (page < 0 || page >= p.n_pages) {
               atomicOr(p.err, ODA_DEVERR_PAGE_RANGE);
               row = p.n_pages * p.Hkv * 16;             // past the pool: the copy fills zeros
             }
-            tma_load_2d(dst + hf * kHalf + pg * 2048, w ? &mv : &mk, hf * 64, (int32_t)row, &sm.kv_full[st]);
+            if (w) tma_load_3d(dst + pg * kV16<TREE>, &mv, 0, (int32_t)row, 0, &sm.kv_full[st]);
+            else tma_load_2d(dst + hf * kHalf + pg * 2048, &mk, hf * 64, (int32_t)row, &sm.kv_full[st]);
           }
         }
         __syncwarp();
@@ -563,7 +574,8 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     if (elect_one()) {
       constexpr uint32_t kIdS = mma_idesc_bf16(128, 128, false), kIdO = mma_idesc_bf16(128, 128, true);
       const uint64_t dq = smem_desc(smem_u32(sq), 16, 1024), dk = smem_desc(smem_u32(skv), 16, 1024);
-      const uint64_t dv = smem_desc(smem_u32(skv), kHalf, 1024);
+      const uint64_t dv = smem_desc(smem_u32(skv), kVHalf<TREE>, 1024);
+      constexpr uint32_t kV = kV16<TREE> >> 4;
       constexpr uint32_t kStep = kStageBytes >> 4;  // of a descriptor's address
       uint32_t st = 0, ph = 0;                      // stage and phase of the next tile in the order of use
       uint32_t np0 = 0, np1 = 0, jobs = 0;          // parity of each slot's weights consumed; of the jobs
@@ -576,10 +588,10 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         tc_fence_after();
         if (nk == 8) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16_ts(tO, tS + k * 8, bv + k * 128, kIdO, acc || k > 0);
+          for (int k = 0; k < 4; ++k) mma_f16_ts(tO, tS + k * 8, bv + k * kV, kIdO, acc || k > 0);
         } else {
 #pragma unroll 1
-          for (int k = 0; k < min(nk, 4); ++k) mma_f16_ts(tO, tS + k * 8, bv + k * 128, kIdO, acc || k > 0);
+          for (int k = 0; k < min(nk, 4); ++k) mma_f16_ts(tO, tS + k * 8, bv + k * kV, kIdO, acc || k > 0);
         }
         ok = mbar_wait_bounded(&sm.p_ready[i][1], np, kWaitNs);
         np ^= 1;
@@ -587,10 +599,10 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         tc_fence_after();
         if (nk == 8) {
 #pragma unroll
-          for (int k = 4; k < 8; ++k) mma_f16_ts(tO, tS + 32 + k * 8, bv + k * 128, kIdO, true);
+          for (int k = 4; k < 8; ++k) mma_f16_ts(tO, tS + 32 + k * 8, bv + k * kV, kIdO, true);
         } else {
 #pragma unroll 1
-          for (int k = 4; k < nk; ++k) mma_f16_ts(tO, tS + 32 + k * 8, bv + k * 128, kIdO, true);
+          for (int k = 4; k < nk; ++k) mma_f16_ts(tO, tS + 32 + k * 8, bv + k * kV, kIdO, true);
         }
       };
       // S_i = Q K^T
@@ -725,7 +737,8 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         const int rows = 16 - (valid & 15);
         for (int z = half * kTile + r; z < rows * 16; z += 2 * kTile) {
           const int row = valid + (z >> 4), ch = z & 15;
-          *reinterpret_cast<uint4*>(skv + st * kStageBytes + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
+          const int at = TREE ? (row >> 4) * kV16<TREE> + (row & 15) * 128 : row * 128;
+          *reinterpret_cast<uint4*>(skv + st * kStageBytes + (ch >> 3) * kVHalf<TREE> + at + (ch & 7) * 16) =
               make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
@@ -1004,7 +1017,7 @@ oda_status encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* d
                   const cuuint32_t* box) {
   EncodeFn enc = get_encode();
   if (!enc) return set_error(ODA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  const cuuint32_t one[3] = {1, 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims,
                          strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1127,14 +1140,17 @@ oda_status launch_tree(oda_ctx* ctx, const oda_kv_layer* layer, const int32_t* p
   p.part_ml = ctx->tile_part_ml;
   p.plan = ctx->tile_plan;
   CUtensorMap mq, mk, mv, mkn, mvn;
-  const cuuint64_t dims[2] = {128, (cuuint64_t)layer->n_pages * cf.n_kv_heads * 16};
-  const cuuint64_t str[1] = {256};
-  const cuuint32_t box[2] = {64, 16};
-  oda_status st = encode(&mk, layer->k, 2, dims, str, box);
-  if (st == ODA_OK) st = encode(&mv, layer->v, 2, dims, str, box);
+  const cuuint64_t pool = (cuuint64_t)layer->n_pages * cf.n_kv_heads * 16;
+  const cuuint64_t kd[2] = {128, pool}, ks[1] = {256}, vd[3] = {64, pool, 2}, vs[2] = {256, 128};
+  const cuuint32_t kb[2] = {64, 16}, vb[3] = {64, 16, 2};
+  oda_status st = encode(&mk, layer->k, 2, kd, ks, kb);
+  if (st == ODA_OK) st = encode(&mv, layer->v, 3, vd, vs, vb);
   if (st == ODA_OK) st = encode_rows(&mq, q, n_rows, cf.n_q_heads, (int64_t)cf.n_q_heads * 128, p.g, p.nt);
   if (st == ODA_OK) st = encode_rows(&mkn, k_new, n_rows, cf.n_kv_heads, (int64_t)cf.n_kv_heads * 128, 1, ODA_MAX_TREE);
-  if (st == ODA_OK) st = encode_rows(&mvn, v_new, n_rows, cf.n_kv_heads, (int64_t)cf.n_kv_heads * 128, 1, ODA_MAX_TREE);
+  const cuuint64_t nd[4] = {64, (cuuint64_t)n_rows, 2, (cuuint64_t)cf.n_kv_heads};
+  const cuuint64_t ns[3] = {(cuuint64_t)cf.n_kv_heads * 256, 128, 256};
+  const cuuint32_t nb[4] = {64, 16, 2, 1};
+  if (st == ODA_OK) st = encode(&mvn, v_new, 4, nd, ns, nb);
   if (st != ODA_OK) return st;
   const int grid = ctx->n_sms;
   tile_attention_kernel<true><<<grid, kThreads, kDynBytes, stream>>>(mq, mk, mv, mkn, mvn, p);
