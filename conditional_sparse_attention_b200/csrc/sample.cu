@@ -5,6 +5,7 @@
 //
 //   1. the maximum (and for a greedy row its lowest index)
 //   2. for top-k and top-p a histogram over the distance d = (max - l) / T, in 512 bins of 1/32
+//      (for a top-k that lies farther, of 1/2 and of 8)
 //   3. it tells closely how far the cut lies (a bin's weights differ by 3%).  Exact counts and masses within
 //      two distances around that (again with others where they miss it) leave a window of at most 1024
 //      values, which go to CTA 0 in index order; it finds the last one kept (by 8 bits of the values at a
@@ -50,7 +51,7 @@ constexpr int kShort = 192;              // listed values that are compared in p
 constexpr int kSeg = 5120;               // values of a CTA above which the cluster grows
 constexpr int kFrac = 43;                // weights are multiples of 2^-43
 constexpr int kCoarse = 512;              // bins of the histogram that aims
-constexpr float kCoarseBins = 32.f;       // bins to a distance of 1
+constexpr float kCoarseBins = 32.f;       // bins to a distance of 1, first
 constexpr int kWant = 900;               // values aimed at in a window
 constexpr float kNear = 3.f;             // distance from which on masses that place a cut are summed in fp32
 
@@ -357,8 +358,8 @@ struct Row {                             // a CTA's view of its row
     if (i < e) v = *reinterpret_cast<const float4*>(x + i);
     l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
   }
-  // The CTA's values by distance, and the mass of those behind the last bin.
-  __device__ void distances() {
+  // The CTA's values by distance, `bins` to a distance of 1, and the mass of those behind the last bin.
+  __device__ void distances(float bins) {
     const int a = min(n, warp * per), e = min(n, a + per);
     float beyond = 0.f;
 #pragma unroll 1
@@ -367,7 +368,7 @@ struct Row {                             // a CTA's view of its row
       load4v(i, e, l);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float d = distance(l[j]), b = d * kCoarseBins;
+        const float d = distance(l[j]), b = d * bins;
         if (b < (float)kCoarse) atomicAdd(&sm.coarse[(int)b], 1u);
         else beyond += exp2_approx(d * -1.4426950408889634f);
       }
@@ -965,11 +966,12 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
     // ---- top-k's count or top-p's mass
     unsigned long long mass = 0;
     const bool by_mass = !by_k;
-    R.distances();
-    cluster.sync();
     // ---- how far that is, to a few values, and a distance on both sides of it.  A bin a thread.
-    float d1, d2;
-    {
+    float d1, d2, bins = kCoarseBins;
+#pragma unroll 1
+    while (true) {
+      R.distances(bins);
+      cluster.sync();
       uint32_t c = 0;
 #pragma unroll
       for (int r = 0; r < kMaxC; ++r)
@@ -986,6 +988,14 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
       const float part = lane < kWarps ? __uint_as_float((uint32_t)sm.wx[lane].a) : 0.f;
       // from the far end, where the weights are small: how much lies behind the cut, and in this bin and behind
       const float all = warp_sum(part), from = all - warp_sum(lane < warp ? part : 0.f) - run + wb;
+      // top-k that reaches behind the last bin (a low temperature): again with wider ones
+      if (by_k && all < (float)kk && bins > 0.1f) {
+        cluster.sync();
+        sm.coarse[tid] = 0;
+        __syncthreads();
+        bins *= 1.f / 16.f;
+        continue;
+      }
       const float behind = by_mass ? (1.f - tp) * (all + beyond) - beyond : all - (float)kk;
       const float at = warp_sum(from - wb > behind ? 1.f : from > behind && wb > 0.f ? (from - behind) / wb : 0.f);
       if (lane == 0) sm.wx[warp].c = __float_as_uint(at);
@@ -995,13 +1005,15 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
       const uint32_t three = __reduce_add_sync(0xffffffffu, fabsf((float)tid + 0.5f - mid) < 1.5f ? c : 0u);
       if (lane == 0 && three) atomicAdd(&sm.around[0], three);
       __syncthreads();
-      const float half = fminf(kCoarseBins, (float)(kWant / 2) * 3.f / (float)max(1u, sm.around[0]));
+      const float half = fminf(fmaxf(bins, 2.f), (float)(kWant / 2) * 3.f / (float)max(1u, sm.around[0]));
       const uint32_t below = __reduce_add_sync(0xffffffffu, (float)tid < mid + half ? c : 0u);
       if (lane == 0 && below) atomicAdd(&sm.around[1], below);
       __syncthreads();
-      d1 = sm.around[1] <= (uint32_t)kList ? 0.f : fmaxf(0.f, mid - half) / kCoarseBins;
-      d2 = (mid + half) / kCoarseBins;
+      const float step = __uint_as_float(0x7f000000u - __float_as_uint(bins));           // 1 / bins, a power of two
+      d1 = sm.around[1] <= (uint32_t)kList ? 0.f : fmaxf(0.f, mid - half) * step;
+      d2 = (mid + half) * step;
       if (p.vocab <= kList) d1 = 0.f, d2 = INFINITY;
+      break;
     }
     // ---- a window of at most kList values that holds the cut
     float near = 0.f, far = INFINITY;    // fewer than the target lie nearer than `near`, enough nearer than `far`

@@ -181,3 +181,11 @@ def test_logits_whose_differences_leave_fp32(ctx, vocab, kw):
     logits = ((r.rand(6, vocab) * 2 - 1) * 3.3e38).astype(np.float32)
     logits[1] = np.where(r.rand(vocab) < 0.5, np.float32(3.4e38), np.float32(-3.4e38))
     _check(ctx, logits, r.rand(6), temperature=1e38, **kw)
+
+
+@pytest.mark.parametrize("temperature", [0.3, 0.05, 0.003, 1e-4])
+@pytest.mark.parametrize("kw", [dict(top_k=50), dict(top_k=900, top_p=0.9999), dict(top_k=5000), dict(top_k=59990)])
+def test_low_temperatures_with_top_k(ctx, temperature, kw):
+    """A top-k that reaches far behind the maximum."""
+    r = np.random.RandomState(5)
+    _check(ctx, r.randn(8, 60000) * 2.5, r.rand(8), temperature=temperature, **kw)
