@@ -64,6 +64,7 @@ struct TileParams {
   int32_t* err;
   int64_t n_rows;
   int n_seqs, Hq, Hkv, g, nt;           // nt = tokens of a slot
+  int nq;                               // tree: nodes of a copy of Q, a divisor of nt
   int local, sinks, window;
   float c;                              // log2(e) / sqrt(128)
   // tree
@@ -506,9 +507,18 @@ tile_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       if (w == 0) {
         if (jobs > 0) ok = mbar_wait_bounded(&sm.q_empty, (jobs - 1) & 1, kWaitNs);
         if (!ok) break;
-        if (lane == 0) {
-          const int slots = jb.n1 > 0 ? 2 : 1;
-          mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(slots * 2 * 128 * p.g * p.nt));
+        const int slots = jb.n1 > 0 ? 2 : 1;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(slots * 2 * 128 * p.g * p.nt));
+        if (TREE) {
+          // A copy a lane (4 nt / nq <= 32 of them): nq nodes' half rows.  Those behind the tree's last node come
+          // from behind the last row, as zeros: rows of zeros cost the tensor cores less power, and the
+          // power cap holds the clock (32 sequences, 16 nodes, on a GPU at its cap: 464 -> 440 us).
+          __syncwarp();
+          const int each = p.nt / p.nq, i = lane / (2 * each), part = (lane >> 1) % each, tok = jb.tok0 + i * p.nt + part * p.nq;
+          if (i < slots)
+            tma_load_3d(sq + i * kStageBytes + (lane & 1) * kHalf + part * p.nq * p.g * 128, &mq, (lane & 1) * 64, jb.h * p.g,
+                        tok < jb.len ? jb.row0 + tok : (int)p.n_rows, &sm.q_full);
+        } else if (lane == 0) {
           for (int i = 0; i < slots; ++i)
             for (int h2 = 0; h2 < 2; ++h2)
               tma_load_3d(sq + i * kStageBytes + h2 * kHalf, &mq, h2 * 64, jb.h * p.g, jb.row0 + jb.tok0 + i * p.nt,
@@ -1117,6 +1127,7 @@ oda_status launch_tree(oda_ctx* ctx, const oda_kv_layer* layer, const int32_t* p
     return set_error(ODA_ERR_INVALID_ARG, "tree: pools, q, k_new, v_new and out must be 16-byte aligned");
   TileParams p = {};
   p.nt = kTile / ctx->g;
+  p.nq = p.nt % 16 ? p.nt : 16;
   const int64_t units = (ODA_MAX_TREE + 2 * p.nt - 1) / (2 * p.nt);
   if ((int64_t)cf.batch * cf.n_kv_heads * units * ((cf.max_pages + 7) / 8 + 1) > (int64_t)INT32_MAX)
     return set_error(ODA_ERR_UNSUPPORTED, "tree: batch * KV heads * max_pages beyond the tile count");
@@ -1145,7 +1156,7 @@ oda_status launch_tree(oda_ctx* ctx, const oda_kv_layer* layer, const int32_t* p
   const cuuint32_t kb[2] = {64, 16}, vb[3] = {64, 16, 2};
   oda_status st = encode(&mk, layer->k, 2, kd, ks, kb);
   if (st == ODA_OK) st = encode(&mv, layer->v, 3, vd, vs, vb);
-  if (st == ODA_OK) st = encode_rows(&mq, q, n_rows, cf.n_q_heads, (int64_t)cf.n_q_heads * 128, p.g, p.nt);
+  if (st == ODA_OK) st = encode_rows(&mq, q, n_rows, cf.n_q_heads, (int64_t)cf.n_q_heads * 128, p.g, p.nq);
   if (st == ODA_OK) st = encode_rows(&mkn, k_new, n_rows, cf.n_kv_heads, (int64_t)cf.n_kv_heads * 128, 1, ODA_MAX_TREE);
   const cuuint64_t nd[4] = {64, (cuuint64_t)n_rows, 2, (cuuint64_t)cf.n_kv_heads};
   const cuuint64_t ns[3] = {(cuuint64_t)cf.n_kv_heads * 256, 128, 256};
