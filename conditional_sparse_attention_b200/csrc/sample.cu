@@ -27,7 +27,7 @@
 // 4500 clocks for the row, 2000 for the maximum, 12000 for step 2, 7000 for a pass of step 3, 2500 to 9000 for
 // CTA 0's part, 13000 for step 4 (where every value survives, the fp64 pipe: some 11 operations a weight at 64
 // lanes a clock and SM).  Two CTAs an SM overlap theirs.  Measured at 151936 values, settings mixed, data not
-// in L2: one row 21 us, 32 rows 38 us, 256 rows 205 us (0.8 TB/s); greedy 256 rows 70 us.
+// in L2: one row 21 us, 32 rows 39 us, 256 rows 193 us (0.8 TB/s); greedy 256 rows 70 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
