@@ -42,8 +42,8 @@ extern "C" {
  *   out = sum_{j in S_t} softmax_j(q . k_j / sqrt(128)) v_j,  S_t = S^F_t (full) or S^L_t (local).
  * q: bf16, head h of row r at q + r*q_stride + h*128; k, v: bf16, KV head c of row r at
  * + r*kv_stride + c*128 (strides in elements, multiples of 8, >= Hq*128 and Hkv*128; so q, k and v
- * may be columns of one projection output); out: bf16 [n_rows][Hq][128].  q, k, v and out 16-byte
- * aligned.  Products of bf16 operands with fp32 sums; softmax statistics fp32; the weights are
+ * may be columns of one projection output); out: bf16 [n_rows][Hq][128], apart from them.  q, k, v and
+ * out 16-byte aligned.  Products of bf16 operands with fp32 sums; softmax statistics fp32; the weights are
  * rounded to bf16 before the product with V, and the output once at the end.  A NaN or infinity in
  * one sequence's rows never reaches another sequence.  Within its own, one of k reaches the rows that see
  * it, as the formula says (NaN, but for a score of -inf beside finite ones, whose weight is 0); one of v
@@ -65,7 +65,7 @@ oda_status oda_attend_local_prompt(oda_ctx* ctx, int32_t n_seqs, int64_t n_rows,
  * child of the last cached position; a parent out of range sets ODA_DEVERR_ROW_RANGE and counts as
  * -1.  Node i reads every cached position, its ancestors and itself.  q: bf16 [n_rows][Hq][128];
  * k_new, v_new: bf16 [n_rows][Hkv][128] (the nodes' own keys and values, never in the cache);
- * out: bf16 [n_rows][Hq][128]; all 16-byte aligned; 1 <= n_rows <= batch*ODA_MAX_TREE (0 nodes:
+ * out: bf16 [n_rows][Hq][128], apart from them; all 16-byte aligned; 1 <= n_rows <= batch*ODA_MAX_TREE (0 nodes:
  * cu_rows all equal).  Rows of skipped sequences are left as they were.  A page-table entry outside
  * the pool sets ODA_DEVERR_PAGE_RANGE, a position outside the table's capacity ODA_DEVERR_POS_RANGE
  * (the sequence is skipped); the outputs of a sequence with a bad page are undefined.  Arithmetic and
