@@ -53,6 +53,7 @@ constexpr int kFrac = 43;                // weights are multiples of 2^-43
 constexpr int kCoarse = 512;              // bins of the histogram that aims
 constexpr float kCoarseBins = 32.f;       // bins to a distance of 1, first
 constexpr int kWant = 900;               // values aimed at in a window
+constexpr int kNone = -2;                // in a token's place: the row has none
 constexpr float kNear = 3.f;             // distance from which on masses that place a cut are summed in fp32
 
 struct SampleParams {
@@ -621,7 +622,7 @@ struct Row {                             // a CTA's view of its row
     return drop;
   }
 
-  // The same for a short list, a thread a value: every thread sums what lies above its own (a list of
+  // The same draw for a short list, a thread a value: every thread sums what lies above its own (a list of
   // 2: 9600 -> 2700 clocks, one of 150: 8200 -> 7200).
   __device__ void draw_short(int m, bool whole, int kk, float tp, float mp, unsigned long long mass, float u, int* token,
                              float* prob) {
@@ -668,6 +669,10 @@ struct Row {                             // a CTA's view of its row
     }
     if (mp > 0.f) keep = keep && x >= fmin((double)mp, 1.0);
     const unsigned long long total = sum(keep ? w : 0ull, &before);
+    if (total == 0) {
+      if (tid == 0) *token = kNone;
+      return;
+    }
     const unsigned long long want = min((unsigned long long)((double)u * (double)total), total - 1);
     if (keep && before <= want && want < before + w) {
       *token = (int)cnt[kList + tid];
@@ -676,7 +681,7 @@ struct Row {                             // a CTA's view of its row
   }
 
   // CTA 0 draws from the m listed values, which hold every cut (`mass`: top-p's total without top-k; `whole`: they
-  // are the row's all).
+  // are the row's all).  One thread gets the token's place; where nothing is left, thread 0 gets kNone.
   __device__ void draw_list(int m, bool whole, int kk, float tp, float mp, unsigned long long mass, float u, int* token,
                             float* prob) {
     if (m <= kShort) return draw_short(m, whole, kk, tp, mp, mass, u, token, prob);
@@ -711,6 +716,10 @@ struct Row {                             // a CTA's view of its row
     __syncthreads();
     const unsigned long long v = lane < kWarps ? sm.w64[lane] : 0ull;
     const unsigned long long before = ws - (w0 + w1) + warp_sum(lane < warp ? v : 0ull), total = warp_sum(v);
+    if (total == 0) {
+      if (tid == 0) *token = kNone;
+      return;
+    }
     const unsigned long long want = min((unsigned long long)((double)u * (double)total), total - 1);
     if (before <= want && want < before + w0 + w1) {
       const bool second = want >= before + w0;
@@ -1091,8 +1100,8 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
         int token = -1;
         float prob = 0.f;
         R.draw_list(m, p.vocab <= kList, by_k ? kk : 0, tp, mp, mass, u, &token, &prob);
-        if (token >= 0) {
-          p.token[row] = token - mis;
+        if (token != -1) {               // this thread's to write
+          p.token[row] = token == kNone ? -1 : token - mis;
           if (p.prob) p.prob[row] = prob;
         }
         return;
@@ -1188,6 +1197,13 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   const unsigned long long theirs = lane < C ? R.remote(lane, t).a : 0ull;
   unsigned long long before = warp_sum(lane < rank ? theirs : 0ull);
   const unsigned long long total = warp_sum(theirs);
+  if (total == 0) {                      // the same for the whole cluster
+    if (rank == 0 && tid == 0) {
+      p.token[row] = -1;
+      if (p.prob) p.prob[row] = 0.f;
+    }
+    return;
+  }
   const unsigned long long want = min((unsigned long long)((double)u * (double)total), total - 1);
   if (want < before || want >= before + here) return;    // the draw is another CTA's
   // ---- the element: the warp's part that holds it, which all warps share out, then the share
