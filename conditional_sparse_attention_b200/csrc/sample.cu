@@ -264,7 +264,8 @@ __device__ __noinline__ CutMass cut_list(Shared& sm, const uint32_t* key, int m,
     const Exchange f = sm.found;
     above = f.a;
     top -= f.c << shift;
-    bot = shift ? max(bot, top - ((1u << shift) - 1u)) : top;
+    const uint32_t width = (1u << shift) - 1u;
+    bot = max(bot, top > width ? top - width : 0u);        // (a bin may reach below key 0: values near the type's lowest)
     if (shift == 0) break;
     shift -= 8;
   }
