@@ -44,10 +44,11 @@ __device__ __forceinline__ uint32_t quantize_row_e4m3(uint32_t w01, uint32_t w23
   if (amax >= 0x1p-80f && amax <= 0x1p100f) {
     // The same roundings by a reciprocal (Markstein): r = RN(1 / b), q = RN(a r), RN(q + r (a - q b)) is RN(a / b)
     // where a - q b is exact.  Here it is for every quotient of 2^-11 or more (s >= 2^-89, so its products with
-    // a quotient's last place reach down to 2^-145); a smaller one is a code of 0 however it is rounded.
+    // a quotient's last place reach down to 2^-145); a smaller one is a code of 0 however it is rounded.  (Its sign
+    // is a's, as a division's: from a = -0 the correction makes +0.)
     auto quotient = [](float a, float by, float r) {
       const float q = a * r;
-      return fmaf(r, fmaf(-q, by, a), q);
+      return copysignf(fmaf(r, fmaf(-q, by, a), q), a);
     };
     s = quotient(amax, 448.0f, 1.0f / 448.0f);
     const float r = __frcp_rn(s);
