@@ -345,7 +345,8 @@ struct Row {                             // a CTA's view of its row
   __device__ unsigned long long sum_a(int t) { return warp_sum(lane < C ? remote(lane, t).a : 0ull); }
   __device__ uint32_t sum_c(int t) { return __reduce_add_sync(0xffffffffu, lane < C ? remote(lane, t).c : 0u); }
 
-  // (max - l) / T; by halves, whose difference cannot overflow
+  // (max - l) / T, never below 0; by halves, whose difference cannot overflow.  NaN where 2 / T is infinite, or 0 for
+  // l = -inf.
   __device__ float distance(float l) const { return fmaf(l, -0.5f, half_max) * inv_half; }
 
   // Four values 32 apart (-inf behind e).  Weights are made four abreast, since one alone is a chain of a
@@ -860,6 +861,14 @@ __device__ __noinline__ Cut general(Row R, int vocab, int kk, float tp, int* tur
   return cut;
 }
 
+// The CTA's values times a power of two.
+__device__ __noinline__ void scale_row(float* x, int n, float by) {
+  __syncthreads();
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n; i += kT) x[i] *= by;
+  __syncthreads();
+}
+
 __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ Shared sm;
@@ -936,7 +945,8 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
   int t = R.exchange({0, 0, best, 0});
   best = __reduce_max_sync(0xffffffffu, lane < C ? R.remote(lane, t).c : 0u);
   // ---- settings
-  const float T = sm.temperature, tp = sm.top_p, mp = sm.min_p;
+  float T = sm.temperature;
+  const float tp = sm.top_p, mp = sm.min_p;
   const int kk = sm.top_k;
   float u = sm.u;
   u = u >= 0.f ? fminf(u, 1.f) : 0.f;
@@ -965,6 +975,13 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleParams p) {
     for (int i = tid; i < n; i += kT) x[i] = x[i] == INFINITY ? 0.f : -INFINITY;
     lmax = 0.f;
     __syncthreads();
+  }
+  if (T < 0x1p-100f && fabsf(lmax) < 0x1p60f) {
+    // Halves of values of such a temperature's size lose bits: logits and temperature times 2^60, which no weight
+    // depends on.  (What becomes -inf by that lies 2^160 T behind the maximum; beyond 2^60 every difference does.)
+    scale_row(x, n, 0x1p60f);
+    lmax *= 0x1p60f;
+    T *= 0x1p60f;
   }
   R.half_max = 0.5f * lmax;
   R.inv_half = 2.f / T;
