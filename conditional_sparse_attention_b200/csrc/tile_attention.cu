@@ -308,11 +308,12 @@ __device__ __forceinline__ void load_cols(uint32_t* v, uint32_t at) {
 
 // 2^x of a pair on the FMA pipe: x = n + f with n whole and |f| <= 1/2, 2^f by the cubic of least
 // relative error on that range (7.5e-5, fitted by reweighted least squares; the weights are then
-// rounded to bf16, 3.9e-3), n added to the exponent.  x is held at -125 from below.
+// rounded to bf16, 3.9e-3), times 2^n made of its exponent's bits.  x is held at -127 from below, where those are 0:
+// a masked column's weight is 0, like the exponential unit's.
 __device__ __forceinline__ void exp2_pair(uint64_t x2, float& a, float& b) {
   f32x2_split(x2, a, b);
-  x2 = f32x2(fmaxf(a, -125.f), fmaxf(b, -125.f));
-  const float kRound = 12582912.f;       // 1.5 * 2^23: adding it rounds to a whole number
+  x2 = f32x2(fmaxf(a, -127.f), fmaxf(b, -127.f));
+  const float kRound = 12583039.f;       // 1.5 * 2^23 + 127: adding it leaves n + 127 in the low bits
   const uint64_t t2 = add_f32x2(x2, f32x2(kRound, kRound));
   const uint64_t n2 = add_f32x2(t2, f32x2(-kRound, -kRound));
   const uint64_t f2 = fma_f32x2(n2, f32x2(-1.f, -1.f), x2);
@@ -321,9 +322,8 @@ __device__ __forceinline__ void exp2_pair(uint64_t x2, float& a, float& b) {
   y2 = fma_f32x2(y2, f2, f32x2(0.99992811f, 0.99992811f));
   float ta, tb;
   f32x2_split(t2, ta, tb);
+  y2 = mul_f32x2(y2, f32x2(__uint_as_float(__float_as_uint(ta) << 23), __uint_as_float(__float_as_uint(tb) << 23)));
   f32x2_split(y2, a, b);
-  a = __uint_as_float(__float_as_uint(a) + (__float_as_uint(ta) << 23));
-  b = __uint_as_float(__float_as_uint(b) + (__float_as_uint(tb) << 23));
 }
 
 // Weights 2^(c v - mc) of 32 columns as bf16 pairs, which take the scores' registers, and their sums
