@@ -315,6 +315,14 @@ def _want(name, t, dtypes, shape=None):
     raise ValueError(f"{name}: expected a contiguous tensor")
 
 
+def _here(*tensors):
+    """Tensors (or None) of the current device, the only one whose memory a call may touch."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"expected tensors of the current device, cuda:{device}, got one of {t.device}")
+
+
 @functools.lru_cache(maxsize=None)
 def _array_type(cls, n):
     return cls * n
@@ -351,6 +359,7 @@ def _attend_prompt(fn, ctx, cu_rows, q, k, v, out, stream):
     if ks != vs:
         raise ValueError("k and v must have the same row stride")
     _want("out", out, _BF16, (n, Hq, 128))
+    _here(cu_rows, q, k, v, out)
     check(fn(ctx.handle, n_cu - 1, n, _p(cu_rows), _p(q), _p(k), _p(v), qs, ks, _p(out),
              _s(stream)))
 
@@ -381,6 +390,7 @@ def oda_attend_full_tree(ctx, layer: OdaKVLayer, page_table, pos, flag, cu_rows,
     _want("k_new", k_new, _BF16, (n, c.n_kv_heads, 128))
     _want("v_new", v_new, _BF16, (n, c.n_kv_heads, 128))
     _want("out", out, _BF16, (n, c.n_q_heads, 128))
+    _here(page_table, pos, flag, cu_rows, parent, q, k_new, v_new, out)
     check(_lib.load().oda_attend_full_tree(ctx.handle, ctypes.byref(layer), _p(page_table), _p(pos), _p(flag), n,
                                            _p(cu_rows), _p(parent), _p(q), _p(k_new), _p(v_new), _p(out),
                                            _s(stream)))
@@ -404,6 +414,7 @@ def _append(fn, cls, ctx, layers, page_table, pos, cu_rows, rows, k_stage, v_sta
         _want("h_prev", h_prev, _F32, (c.batch, c.head_in_dim))
     if pos_next is not None:
         _want("pos_next", pos_next, _I32, (c.batch,))
+    _here(page_table, pos, cu_rows, rows, k_stage, v_stage, h_stage, h_prev, pos_next)
     n_rows = n_stage if rows is None else int(rows.shape[0])
     check(fn(ctx.handle, arr, len(layers), _p(page_table), _p(pos), n_rows, n_stage, _p(cu_rows), _p(rows),
              _p(k_stage), _p(v_stage), _p(h_stage), _p(h_prev), _p(pos_next), _s(stream)))
@@ -438,6 +449,7 @@ def oda_sample(ctx, logits, u, token, temperature=None, top_k=None, top_p=None, 
                         ("min_p", min_p, _F32), ("prob", prob, _F32)):
         if t is not None:
             _want(name, t, dt, shape)
+    _here(logits, u, token, temperature, top_k, top_p, min_p, prob)
     stride = logits.stride(0) if n > 1 else vocab
     check(_lib.load().oda_sample(ctx.handle, n, vocab, stride, _p(logits), _p(temperature), _p(top_k), _p(top_p),
                                  _p(min_p), _p(u), _p(token), _p(prob), _s(stream)))
