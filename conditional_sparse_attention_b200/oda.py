@@ -29,9 +29,16 @@ def _p(t) -> ctypes.c_void_p:
     return _c(t.data_ptr())
 
 
+# The current stream's handle without a Stream object, which costs 3 us a call.  The name is not public: where a
+# PyTorch lacks it, the public call serves.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _s(stream) -> ctypes.c_void_p:
-    if stream is None:                   # the current stream's handle, without a Stream object (3 us a call)
-        return _c(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    if stream is None:
+        if _raw_stream is None:
+            return _c(torch.cuda.current_stream().cuda_stream)
+        return _c(_raw_stream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return _c(stream)
     return _c(stream.cuda_stream)
