@@ -1091,7 +1091,7 @@ oda_status launch_prompt(oda_ctx* ctx, int n_seqs, int64_t n_rows, const int32_t
   if (!cu_rows || !q || !k || !v || !out) return set_error(ODA_ERR_INVALID_ARG, "prompt: null pointer argument");
   if (n_seqs < 1 || n_seqs > ODA_MAX_BATCH)
     return set_error(ODA_ERR_INVALID_ARG, "prompt: n_seqs must be 1..%d", ODA_MAX_BATCH);
-  if (n_rows < 1 || n_rows * (int64_t)cf.n_q_heads > INT32_MAX)
+  if (n_rows < 1 || n_rows > INT32_MAX / cf.n_q_heads)
     return set_error(ODA_ERR_INVALID_ARG, "prompt: n_rows out of range (%lld)", (long long)n_rows);
   if (q_stride < (int64_t)cf.n_q_heads * 128 || kv_stride < (int64_t)cf.n_kv_heads * 128 || (q_stride & 7) ||
       (kv_stride & 7) || q_stride > (int64_t(1) << 32) || kv_stride > (int64_t(1) << 32))
@@ -1130,7 +1130,7 @@ oda_status launch_tree(oda_ctx* ctx, const oda_kv_layer* layer, const int32_t* p
   const oda_config& cf = ctx->cfg;
   if (!layer || !layer->k || !layer->v || !page_table || !pos || !cu_rows || !parent || !q || !k_new || !v_new || !out)
     return set_error(ODA_ERR_INVALID_ARG, "tree: null pointer argument");
-  if (layer->n_pages <= 0 || (layer->n_pages + 1) * (int64_t)cf.n_kv_heads * 16 > INT32_MAX)
+  if (layer->n_pages <= 0 || layer->n_pages >= INT32_MAX / (cf.n_kv_heads * (int64_t)16))
     return set_error(ODA_ERR_INVALID_ARG, "tree: n_pages out of range (%lld)", (long long)layer->n_pages);
   if (n_rows < 1 || n_rows > (int64_t)cf.batch * ODA_MAX_TREE)
     return set_error(ODA_ERR_INVALID_ARG, "tree: n_rows must be 1..batch * %d", ODA_MAX_TREE);
