@@ -503,9 +503,12 @@ struct Row {                             // a CTA's view of its row
 
   // Numbers, and where asked masses, of all values nearer than d1 and than d2 (>= d1), over the cluster: a, c
   // and b, d of the result; m the mass of all.  (Each warp's stay in sm.wx, each CTA's in buffer *t.)
-  // These masses place a cut: those beyond kNear are summed in fp32 (in a fixed order; below 0.05 of the
-  // largest weight, 2^-22 of error a weight, averaged over thousands of them).  A draw's own masses are
-  // exact.
+  // These masses place a cut: those beyond kNear are summed in fp32, in a fixed order.  A weight there is off by at
+  // most (4.2 d + 4) 2^-24 of itself (2 / T, the difference, the distance, log2(e) and the exponent round once each,
+  // the exponential 2^-22), a lane's sum of n / 512 of them by half as many 2^-24.  What all of them share in it, as
+  // 2 / T's rounding, moves the cut by (mass up to d = 3) (1 - top_p), at most 1/4, of it.  Measured over 38000 rows
+  // of up to 262144 values, most of them with half their mass at distances 9..13.5: 1.5e-7 of the mass.  A draw's own
+  // masses are exact.
   __device__ Exchange within(float d1, float d2, bool mass, int* t) {
     const int a = min(n, warp * per), e = min(n, a + per);
     Exchange v = {};
