@@ -1536,24 +1536,6 @@ __global__ void index_positions_kernel(const int32_t* pos, const int32_t* flag, 
   counts[b] = min(n, cap);
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                              CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn get_encode() {
-  static EncodeFn fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeFn>(ptr);
-  }
-  return fn;
-}
-
 // Tensor maps of one layer's pools [n_pages][Hkv][16][128] bf16, seen as rows of 128 values
 // split into two 64-value (128-byte) halves: dims {64, rows, 2} with byte strides {256, 128},
 // box {64, 16, 2}, 128-byte swizzle, so a box lands in shared memory as [half][row][64].
@@ -1596,6 +1578,19 @@ oda_status encode_kv(CUtensorMap* a, CUtensorMap* b, int* single, const void* k,
 }
 
 }  // namespace
+
+EncodeFn get_encode() {
+  static EncodeFn fn = nullptr;
+  if (!fn) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(ptr);
+  }
+  return fn;
+}
 
 // Stride of the full-set CTA -> range permutation: near a quarter of the grid, coprime to it.
 int cta_stride(int grid) {

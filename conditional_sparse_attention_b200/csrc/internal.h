@@ -60,6 +60,13 @@ oda_status check_cuda(cudaError_t e, const char* what);
 // of oda_config except head_in_dim, theta and overlap_layers.
 oda_status validate_attention_config(const oda_config& c, const char* who);
 
+// The driver's encoder of tensor maps, looked up once (NULL: not available).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+EncodeFn get_encode();
+
 // Where one layer's cached pages live: fmt 0 = bf16 K and V pools (k, v), fmt 1 = fp8 page
 // blocks (k; v unused).
 struct KvPool {
