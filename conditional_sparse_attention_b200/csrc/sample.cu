@@ -5,7 +5,7 @@
 //
 //   1. the maximum (and for a greedy row its lowest index)
 //   2. for top-k and top-p a histogram over the distance d = (max - l) / T, in 512 bins of 1/32
-//      (for a top-k that lies farther, of 1/2 and of 8)
+//      (for a top-k that lies farther, of 1/2, of 8 and of 128)
 //   3. it tells closely how far the cut lies (a bin's weights differ by 3%).  Exact counts and masses within
 //      two distances around that (again with others where they miss it) leave a window of at most 1024
 //      values, which go to CTA 0 in index order; it finds the last one kept (by 8 bits of the values at a
@@ -27,7 +27,7 @@
 // 4500 clocks for the row, 2000 for the maximum, 12000 for step 2, 7000 for a pass of step 3, 2500 to 9000 for
 // CTA 0's part, 13000 for step 4 (where every value survives, the fp64 pipe: some 11 operations a weight at 64
 // lanes a clock and SM).  Two CTAs an SM overlap theirs.  Measured at 151936 values, settings mixed, data not
-// in L2: one row 21 us, 32 rows 39 us, 256 rows 193 us (0.8 TB/s); greedy 256 rows 70 us.
+// in L2: one row 18 to 25 us, 32 rows 40 us, 256 rows 190 to 197 us (0.8 TB/s); greedy 256 rows 70 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>

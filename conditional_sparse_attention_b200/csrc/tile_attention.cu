@@ -27,12 +27,12 @@
 // Bounds and measurements (B200; copies at 6548 GB/s, library products at 1624 TFLOP/s):
 //   prompts: the matrix products and, as long, the exponentials of a step, each waiting for the other; in
 //     repeated calls the power cap (the same time with any share of the exponentials on the FMA pipe).  One
-//     prompt of 8192, 32/8 heads, full set: 438 us alone, 505 to 528 repeated (1040 to 1090 TFLOP/s, 64 to 67%);
-//     local set (4 + 2048): 231 us alone, 269 to 281 repeated (the tiles at the window's two ends and the sinks'
-//     tile are partly masked: 18 tiles for 16).  One token: 7.4 us; 512 tokens, 16/8 heads: 14.5 us.
-//   trees: the cache's bytes while a KV head has few rows (32 sequences of 2000..32768, 16 nodes, 16/8 heads: 385 us
-//     alone, 6.1 TB/s, 418 to 441 repeated), then the products and the power of both (4 of 131072, 64 nodes, 32/8
-//     heads: 515 us alone, 586 to 654 repeated).  A chain of 5 over 4096 positions: 20 us, of which the join is 5.
+//     prompt of 8192, 32/8 heads, full set: 435 to 475 us alone, 500 to 528 repeated (1040 to 1100 TFLOP/s, 64 to 68%);
+//     local set (4 + 2048): 260 us alone, 263 to 281 repeated (the tiles at the window's two
+//     ends and the sinks' tile are partly masked: 18 tiles for 16).  One token: 7.3 us; 512 tokens, 16/8 heads: 14.4 us.
+//   trees: the cache's bytes while a KV head has few rows (32 sequences of 2000..32768, 16 nodes, 16/8 heads: 387 us
+//     alone, 6.1 TB/s, 393 to 441 repeated), then the products and the power of both (4 of 131072, 64 nodes, 32/8
+//     heads: 514 us alone, 582 to 654 repeated).  A chain of 5 over 4096 positions: 20 us, of which the join is 5.
 #include <algorithm>
 #include <cmath>
 #include <cstring>

@@ -47,7 +47,9 @@ extern "C" {
  * rounded to bf16 before the product with V, and the output once at the end.  A NaN or infinity in
  * one sequence's rows never reaches another sequence.  Within its own, one of k reaches the rows that see
  * it, as the formula says (NaN, but for a score of -inf beside finite ones, whose weight is 0); one of v
- * makes every row that sees it NaN and may make others NaN. */
+ * makes every row that sees it NaN and may make others NaN.  A finite v in a place that a row does not see has
+ * weight 0.  The sums of weights (up to 2^8 each) times v are held unnormalised: over n positions, v beyond
+ * 2^119 / n may overflow in a row that sees it. */
 oda_status oda_attend_full_prompt(oda_ctx* ctx, int32_t n_seqs, int64_t n_rows,
                                   const int32_t* cu_rows, const void* q, const void* k,
                                   const void* v, int64_t q_stride, int64_t kv_stride, void* out,
